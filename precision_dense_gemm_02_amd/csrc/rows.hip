@@ -1,0 +1,168 @@
+// C entry points of the row kernels (include/lpgemm_moe.h): residual +
+// RMSNorm and silu(gate) * up with int8 rows, MXFP4 quantisation and its
+// inverse.
+#include "../../include/lpgemm_moe.h"
+#include "dispatch.hpp"
+#include "row_kernels.hpp"
+
+using namespace lpgemm;
+
+namespace {
+
+bool is_16bit(lpgemm_type t) { return t == LPGEMM_F16 || t == LPGEMM_BF16; }
+
+lpgemm_status enqueue(const void* fn, int64_t grid, int threads, void* args, hipStream_t stream) {
+  void* kargs[] = {args};
+  return hipLaunchKernel(fn, dim3((unsigned)grid), dim3(threads), kargs, 0, stream) == hipSuccess
+             ? LPGEMM_SUCCESS
+             : LPGEMM_ERROR_LAUNCH;
+}
+
+// The kernel for rows of K values: in registers up to 16384 values, a
+// wavefront per row once the rows fill the SIMDs (up to 8192 values), else a
+// workgroup per row.
+template <typename T, bool NORM>
+lpgemm_status run_rows(RowArgs& p, int cu_count, hipStream_t stream) {
+  const int K = p.K;
+  if (K == 0 || K > 16384) return enqueue((const void*)&rows_int8_long<T, NORM>, p.M, 1024, &p, stream);
+  const bool wide = p.M < 4 * (int64_t)cu_count || K > 8192;
+  const int nc = (K / 8 + (wide ? 255 : 63)) / (wide ? 256 : 64);
+  const void* fn;
+  if (wide)
+    fn = nc <= 1   ? (const void*)&rows_int8_regs<T, NORM, 4, 1>
+         : nc <= 2 ? (const void*)&rows_int8_regs<T, NORM, 4, 2>
+         : nc <= 4 ? (const void*)&rows_int8_regs<T, NORM, 4, 4>
+                   : (const void*)&rows_int8_regs<T, NORM, 4, 8>;
+  else
+    fn = nc <= 1   ? (const void*)&rows_int8_regs<T, NORM, 1, 1>
+         : nc <= 2 ? (const void*)&rows_int8_regs<T, NORM, 1, 2>
+         : nc <= 4 ? (const void*)&rows_int8_regs<T, NORM, 1, 4>
+         : nc <= 8 ? (const void*)&rows_int8_regs<T, NORM, 1, 8>
+                   : (const void*)&rows_int8_regs<T, NORM, 1, 16>;
+  return enqueue(fn, wide ? p.M : ((int64_t)p.M + 3) / 4, 256, &p, stream);
+}
+
+bool bad_stride(int64_t stride, int64_t least) { return stride < least || stride % 8 != 0; }
+
+}  // namespace
+
+extern "C" {
+
+lpgemm_status lpgemm_add_rmsnorm_quantize(int64_t M, int64_t K, lpgemm_type type, const void* X, int64_t x_stride,
+                                          const void* R, int64_t r_stride, const void* weight, float eps, void* H,
+                                          int64_t h_stride, int8_t* Q, float* row_scale, hipStream_t stream) {
+  if (M < 0 || K < 0 || M > INT32_MAX || !is_16bit(type) || !(eps >= 0.f)) return LPGEMM_ERROR_INVALID_VALUE;
+  if (K % 8 != 0 || K > LPGEMM_MAX_K_QUANT) return LPGEMM_ERROR_UNSUPPORTED_SHAPE;
+  if (bad_stride(x_stride, K) || (R && bad_stride(r_stride, K)) || (H && bad_stride(h_stride, K)))
+    return LPGEMM_ERROR_UNSUPPORTED_SHAPE;
+  if (M == 0) return LPGEMM_SUCCESS;
+  if (!row_scale || (K > 0 && (!X || !weight || !Q))) return LPGEMM_ERROR_INVALID_VALUE;
+  if (!aligned4(row_scale)) return LPGEMM_ERROR_MISALIGNED;
+  if (K > 0 && (!aligned16(X) || !aligned16(R) || !aligned16(weight) || !aligned16(H) || !aligned16(Q)))
+    return LPGEMM_ERROR_MISALIGNED;
+  DeviceInfo dev;
+  const lpgemm_status st = current_device(dev);
+  if (st != LPGEMM_SUCCESS) return st;
+  RowArgs p{};
+  p.X = static_cast<const uint8_t*>(X);
+  p.R = static_cast<const uint8_t*>(R);
+  p.weight = static_cast<const uint8_t*>(weight);
+  p.H = static_cast<uint8_t*>(H);
+  p.Q = Q;
+  p.scale = row_scale;
+  p.x_stride = 2 * x_stride;
+  p.r_stride = 2 * r_stride;
+  p.h_stride = 2 * h_stride;
+  p.M = (int)M;
+  p.K = (int)K;
+  p.eps = eps;
+  return type == LPGEMM_F16 ? run_rows<TypeF16, true>(p, dev.cu_count, stream)
+                            : run_rows<TypeBF16, true>(p, dev.cu_count, stream);
+}
+
+lpgemm_status lpgemm_silu_mul_quantize(int64_t M, int64_t K, lpgemm_type type, const void* X, int64_t x_stride,
+                                       int8_t* Q, float* row_scale, hipStream_t stream) {
+  if (M < 0 || K < 0 || M > INT32_MAX || !is_16bit(type)) return LPGEMM_ERROR_INVALID_VALUE;
+  if (K % 8 != 0 || K > LPGEMM_MAX_K_QUANT) return LPGEMM_ERROR_UNSUPPORTED_SHAPE;
+  if (bad_stride(x_stride, 2 * K)) return LPGEMM_ERROR_UNSUPPORTED_SHAPE;
+  if (M == 0) return LPGEMM_SUCCESS;
+  if (!row_scale || (K > 0 && (!X || !Q))) return LPGEMM_ERROR_INVALID_VALUE;
+  if (!aligned4(row_scale)) return LPGEMM_ERROR_MISALIGNED;
+  if (K > 0 && (!aligned16(X) || !aligned16(Q))) return LPGEMM_ERROR_MISALIGNED;
+  DeviceInfo dev;
+  const lpgemm_status st = current_device(dev);
+  if (st != LPGEMM_SUCCESS) return st;
+  RowArgs p{};
+  p.X = static_cast<const uint8_t*>(X);
+  p.Q = Q;
+  p.scale = row_scale;
+  p.x_stride = 2 * x_stride;
+  p.M = (int)M;
+  p.K = (int)K;
+  return type == LPGEMM_F16 ? run_rows<TypeF16, false>(p, dev.cu_count, stream)
+                            : run_rows<TypeBF16, false>(p, dev.cu_count, stream);
+}
+
+// The MXFP4 kernels index a launch's chunks of 8 values in 32 bits; more
+// rows than that go out in several launches.
+static int64_t rows_per_launch(int64_t chunks) { return ((int64_t)1 << 31) / chunks; }
+
+lpgemm_status lpgemm_quantize_mxfp4(int64_t rows, int64_t K, lpgemm_type type, const void* X, int64_t x_stride,
+                                    uint8_t* codes, uint8_t* scales, hipStream_t stream) {
+  if (rows < 0 || K < 0 || rows > INT32_MAX || !is_16bit(type)) return LPGEMM_ERROR_INVALID_VALUE;
+  if (K % 32 != 0 || K > LPGEMM_MAX_K_MXFP4 || bad_stride(x_stride, K)) return LPGEMM_ERROR_UNSUPPORTED_SHAPE;
+  if (rows == 0 || K == 0) return LPGEMM_SUCCESS;
+  if (!X || !codes || !scales) return LPGEMM_ERROR_INVALID_VALUE;
+  if (!aligned16(X) || !aligned16(codes) || !aligned16(scales)) return LPGEMM_ERROR_MISALIGNED;
+  DeviceInfo dev;
+  lpgemm_status st = current_device(dev);
+  if (st != LPGEMM_SUCCESS) return st;
+  const void* fn = type == LPGEMM_F16 ? (const void*)&quantize_mxfp4_kernel<TypeF16>
+                                      : (const void*)&quantize_mxfp4_kernel<TypeBF16>;
+  const int64_t chunks = K / 8, stride = LPGEMM_MXFP4_SCALE_STRIDE(K), most = rows_per_launch(chunks);
+  for (int64_t r = 0; r < rows && st == LPGEMM_SUCCESS; r += most) {
+    const int64_t n = rows - r < most ? rows - r : most;
+    Mxfp4Args p{};
+    p.X = static_cast<const uint8_t*>(X) + 2 * r * x_stride;
+    p.codes = codes + r * (K / 2);
+    p.scales = scales + r * stride;
+    p.x_stride = 2 * x_stride;
+    p.chunks = (int)chunks;
+    p.scale_stride = (int)stride;
+    p.total = (uint32_t)(n * chunks);
+    st = enqueue(fn, (n * chunks + 255) / 256, 256, &p, stream);
+  }
+  return st;
+}
+
+lpgemm_status lpgemm_dequantize_mxfp4(int64_t rows, int64_t K, const uint8_t* codes, const uint8_t* scales,
+                                      lpgemm_type type, void* Y, hipStream_t stream) {
+  if (rows < 0 || K < 0 || rows > INT32_MAX || !(is_16bit(type) || type == LPGEMM_F32))
+    return LPGEMM_ERROR_INVALID_VALUE;
+  if (K % 32 != 0 || K > LPGEMM_MAX_K_MXFP4) return LPGEMM_ERROR_UNSUPPORTED_SHAPE;
+  if (rows == 0 || K == 0) return LPGEMM_SUCCESS;
+  if (!codes || !scales || !Y) return LPGEMM_ERROR_INVALID_VALUE;
+  if (!aligned16(codes) || !aligned16(scales) || !aligned16(Y)) return LPGEMM_ERROR_MISALIGNED;
+  DeviceInfo dev;
+  lpgemm_status st = current_device(dev);
+  if (st != LPGEMM_SUCCESS) return st;
+  const void* fn = type == LPGEMM_F32   ? (const void*)&dequantize_mxfp4_kernel<0>
+                   : type == LPGEMM_F16 ? (const void*)&dequantize_mxfp4_kernel<1>
+                                        : (const void*)&dequantize_mxfp4_kernel<2>;
+  const int64_t chunks = K / 8, stride = LPGEMM_MXFP4_SCALE_STRIDE(K), most = rows_per_launch(chunks);
+  const int64_t size = type == LPGEMM_F32 ? 4 : 2;
+  for (int64_t r = 0; r < rows && st == LPGEMM_SUCCESS; r += most) {
+    const int64_t n = rows - r < most ? rows - r : most;
+    Dequant4Args p{};
+    p.codes = codes + r * (K / 2);
+    p.scales = scales + r * stride;
+    p.Y = static_cast<uint8_t*>(Y) + r * K * size;
+    p.chunks = (int)chunks;
+    p.scale_stride = (int)stride;
+    p.total = (uint32_t)(n * chunks);
+    st = enqueue(fn, (n * chunks + 255) / 256, 256, &p, stream);
+  }
+  return st;
+}
+
+}  // extern "C"

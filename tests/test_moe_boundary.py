@@ -1,0 +1,143 @@
+"""The expert-layer entry points without a GPU: exported, and refusing bad
+arguments on the host before any HIP call (fake pointers are never
+dereferenced by validation); then the Python binding's own refusals."""
+import re
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import precision_dense_gemm_02_amd as lp  # noqa: E402
+from precision_dense_gemm_02_amd import _binding as b  # noqa: E402
+from precision_dense_gemm_02_amd import _moe  # noqa: E402
+
+P = 0x10000           # 16-byte aligned, never dereferenced
+INVALID, MISALIGNED, SHAPE = b.LPGEMM_ERROR_INVALID_VALUE, b.LPGEMM_ERROR_MISALIGNED, b.LPGEMM_ERROR_UNSUPPORTED_SHAPE
+HEADER = b.HEADER_PATH.replace("lpgemm.h", "lpgemm_moe.h")
+
+DEFAULTS = {
+    "lpgemm_add_rmsnorm_quantize": dict(M=4, K=64, type=1, X=P, x_stride=64, R=P, r_stride=64, weight=P, eps=1e-6,
+                                        H=P, h_stride=64, Q=P, row_scale=P),
+    "lpgemm_silu_mul_quantize": dict(M=4, K=64, type=2, X=P, x_stride=128, Q=P, row_scale=P),
+    "lpgemm_quantize_mxfp4": dict(rows=4, K=64, type=1, X=P, x_stride=64, codes=P, scales=P),
+    "lpgemm_dequantize_mxfp4": dict(rows=4, K=64, codes=P, scales=P, type=0, Y=P),
+    "lpgemm_mxfp4": dict(M=4, N=4, K=64, A=P, A_scale=P, B=P, B_scale=P, type=0, C=P),
+    "lpgemm_i8_dequant_grouped": dict(rows=4, groups=2, N=4, K=64, a_rows=3, A=P, B=P, offsets=P, row_index=P,
+                                      row_scale=P, col_scale=P, type=0, C=P),
+    "lpgemm_f16_grouped": dict(rows=4, groups=2, N=4, K=64, a_rows=3, A=P, B=P, offsets=P, row_index=P, type=0, C=P),
+    "lpgemm_mxfp4_grouped": dict(rows=4, groups=2, N=4, K=64, a_rows=3, A=P, A_scale=P, B=P, B_scale=P, offsets=P,
+                                 row_index=P, type=0, C=P),
+}
+GROUPED = ("lpgemm_i8_dequant_grouped", "lpgemm_f16_grouped", "lpgemm_mxfp4_grouped")
+
+
+def call(name, **kw):
+    args = dict(DEFAULTS[name])
+    assert set(kw) <= set(args), kw
+    args.update(kw)
+    return _moe._function(name)(*args.values(), None)
+
+
+def test_exports_every_declared_symbol():
+    text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+    names = re.findall(r"^lpgemm_status\s+(lpgemm_\w+)\s*\(", text, flags=re.M)
+    assert set(names) == set(DEFAULTS) == set(_moe._SIGNATURES)
+    for n in names:
+        assert hasattr(b.load_library(), n)
+        args = re.search(n + r"\s*\((.*?)\)\s*;", text, flags=re.S).group(1)
+        declared = [re.search(r"(\w+)$", a.strip()).group(1) for a in args.split(",")]
+        assert declared == [*DEFAULTS[n], "stream"], n
+
+
+@pytest.mark.parametrize("name", sorted(DEFAULTS))
+def test_sizes(name):
+    for size in set(DEFAULTS[name]) & {"M", "N", "K", "rows", "groups", "a_rows"}:
+        assert call(name, **{size: -8}) == INVALID, size
+    for size in set(DEFAULTS[name]) & {"M", "N", "rows", "a_rows"}:
+        assert call(name, **{size: 2 ** 31}) == INVALID, size
+    assert call(name, type=3) == INVALID and call(name, type=-1) == INVALID
+    if name in ("lpgemm_add_rmsnorm_quantize", "lpgemm_silu_mul_quantize", "lpgemm_quantize_mxfp4"):
+        assert call(name, type=0) == INVALID        # 16-bit inputs only
+
+
+@pytest.mark.parametrize("name,bad_k", [
+    ("lpgemm_add_rmsnorm_quantize", [4, 12, 1048584]), ("lpgemm_silu_mul_quantize", [4, 12, 1048584]),
+    ("lpgemm_quantize_mxfp4", [16, 48, 1048608]), ("lpgemm_dequantize_mxfp4", [16, 48, 1048608]),
+    ("lpgemm_mxfp4", [16, 48, 1048608]), ("lpgemm_mxfp4_grouped", [16, 48, 1048608]),
+    ("lpgemm_i8_dequant_grouped", [8, 24, 131072]), ("lpgemm_f16_grouped", [4, 12, 1048584])])
+def test_unsupported_k(name, bad_k):
+    for K in bad_k:
+        strides = {s: 4 * K for s in ("x_stride", "r_stride", "h_stride") if s in DEFAULTS[name]}
+        assert call(name, K=K, **strides) == SHAPE, K
+
+
+@pytest.mark.parametrize("name,stride", [
+    ("lpgemm_add_rmsnorm_quantize", "x_stride"), ("lpgemm_add_rmsnorm_quantize", "r_stride"),
+    ("lpgemm_add_rmsnorm_quantize", "h_stride"), ("lpgemm_silu_mul_quantize", "x_stride"),
+    ("lpgemm_quantize_mxfp4", "x_stride")])
+def test_strides(name, stride):
+    least = DEFAULTS[name][stride]
+    for bad in (least - 8, 0, -least, least + 4):
+        assert call(name, **{stride: bad}) == SHAPE, bad
+
+
+@pytest.mark.parametrize("name", sorted(DEFAULTS))
+def test_null_and_misaligned_pointers(name):
+    optional = {"R", "H", "row_index"}
+    for k, v in DEFAULTS[name].items():
+        if v != P:
+            continue
+        if k not in optional:
+            assert call(name, **{k: None}) == INVALID, k
+        by = 2 if k in ("offsets", "row_index") or (k in ("row_scale", "col_scale")) else 8
+        assert call(name, **{k: P + by}) == MISALIGNED, k
+
+
+@pytest.mark.parametrize("name", GROUPED)
+def test_grouped_rules(name):
+    # without a row_index there is one row of A per row of C
+    assert call(name, row_index=None) == INVALID
+    assert call(name, groups=65537) == SHAPE
+    # gathered tokens stay below 2 GiB
+    per = {"lpgemm_i8_dequant_grouped": 4096, "lpgemm_f16_grouped": 2048, "lpgemm_mxfp4_grouped": 8192}[name]
+    assert call(name, K=per, a_rows=2 ** 19) == SHAPE
+    # (K = 0 is an empty sum; it still needs C, the offsets and int8's scales)
+    assert call(name, K=0, C=None) == INVALID
+    assert call(name, K=0, offsets=None) == INVALID
+    if name == "lpgemm_i8_dequant_grouped":
+        assert call(name, K=0, col_scale=None) == INVALID
+        assert call(name, K=0, row_scale=None) == INVALID
+
+
+@pytest.mark.parametrize("name", sorted(DEFAULTS))
+def test_empty_problems_read_nothing(name):
+    nothing = {k: None for k, v in DEFAULTS[name].items() if v == P and k != "row_index"}
+    for size in set(DEFAULTS[name]) & {"M", "N", "rows", "groups"}:
+        assert call(name, **{size: 0}, **nothing) == 0, size
+        # the shape rules still hold
+        assert call(name, **{size: 0}, K=44, **nothing) == SHAPE
+
+
+def test_eps():
+    assert call("lpgemm_add_rmsnorm_quantize", eps=-1.0) == INVALID
+    assert call("lpgemm_add_rmsnorm_quantize", eps=float("nan")) == INVALID
+
+
+def test_scale_stride():
+    assert [lp.mxfp4_scale_stride(k) for k in (0, 32, 480, 512, 544, 2880, 4096)] == [0, 16, 16, 16, 32, 96, 128]
+
+
+def test_binding_refuses_host_tensors_and_types():
+    x = torch.zeros(4, 64, dtype=torch.float16)
+    w = torch.zeros(64, dtype=torch.float16)
+    for f in (lambda: lp.add_rmsnorm_quantize(x, w, 1e-6), lambda: lp.silu_mul_quantize(x), lambda: lp.quantize_mxfp4(x)):
+        with pytest.raises(ValueError, match="GPU"):
+            f()
+    with pytest.raises(TypeError):
+        lp.quantize_mxfp4(x.float())
+    with pytest.raises(TypeError):
+        lp.silu_mul_quantize([1, 2])
+    with pytest.raises(TypeError):
+        lp.gemm_f16_grouped(x.float(), x[None], None)
+    with pytest.raises(AttributeError):
+        lp.no_such_operator
