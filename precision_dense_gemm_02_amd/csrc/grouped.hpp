@@ -11,27 +11,25 @@ namespace lpgemm {
 
 // Kernels of the grouped products.
 enum GroupedCfg {
-  GCFG_SKINNY_8 = 0,    // 8 rows x 32 columns, waves split K
-  GCFG_SKINNY_16 = 1,
-  GCFG_SKINNY_32 = 2,
-  GCFG_64x128 = 3,
-  GCFG_128x128 = 4,
-  GCFG_256x256 = 5,
-  GCFG_COUNT = 6
+  GCFG_SKINNY_8_DEEP = 0,  // 8 rows x 32 columns, waves split K, ring of 3 blocks
+  GCFG_SKINNY_8 = 1,       // ... ring of 2 blocks (more workgroups per CU)
+  GCFG_SKINNY_16 = 2,      // 16 rows
+  GCFG_SKINNY_32 = 3,      // 32 rows
+  GCFG_64x64_S4 = 4,       // 64 x 64 tiles, 4 stages
+  GCFG_64x64_S2 = 5,       // ... 2 stages (more workgroups per CU)
+  GCFG_64x128 = 6,
+  GCFG_128x128 = 7,
+  GCFG_256x256 = 8,
+  GCFG_COUNT = 9
 };
 
 inline int grouped_tile_rows(int cfg) {
-  switch (cfg) {
-    case GCFG_SKINNY_8: return 8;
-    case GCFG_SKINNY_16: return 16;
-    case GCFG_SKINNY_32: return 32;
-    case GCFG_64x128: return 64;
-    case GCFG_128x128: return 128;
-    default: return 256;
-  }
+  constexpr int rows[GCFG_COUNT] = {8, 8, 16, 32, 64, 64, 64, 128, 256};
+  return rows[cfg];
 }
 inline int grouped_tile_cols(int cfg) {
-  return cfg <= GCFG_SKINNY_32 ? 32 : (cfg <= GCFG_128x128 ? 128 : 256);
+  constexpr int cols[GCFG_COUNT] = {32, 32, 32, 32, 64, 64, 128, 128, 256};
+  return cols[cfg];
 }
 
 // The most row tiles of `tile` rows that `rows` rows in `groups` groups can
@@ -41,13 +39,55 @@ inline int64_t grouped_max_tiles(int64_t rows, int64_t groups, int tile) {
   return (rows + used * (tile - 1)) / tile;
 }
 
-inline GroupedCfg choose_grouped(int64_t rows, int64_t groups, int64_t N, int cu_count) {
+// The kernel for the sizes.  How the rows fall on the groups is known on the
+// device only; the choice goes by the mean, and by how many tiles the rows
+// would make if half the groups ended in a tile of their own.  Measured at
+// 250 sizes of one group (1 to 4096 rows) and of 8 to 128 groups (1 to 2048
+// tokens, 2 or 8 experts each), N = 768 to 14336, K = 2048 to 14336 (graph
+// replay, one MI355X; the figures at each rule are us with the kernel it
+// takes against the next best).
+inline GroupedCfg choose_grouped(int kind, int64_t rows, int64_t groups, int64_t N, int cu_count) {
   const int64_t used = groups < rows ? groups : rows;
   const int64_t mean = (rows + used - 1) / used;
-  if (mean <= 32) return rows <= 8 ? GCFG_SKINNY_8 : (rows <= 16 ? GCFG_SKINNY_16 : GCFG_SKINNY_32);
-  if (mean <= 64) return GCFG_64x128;
-  if (mean >= 192 && 2 * used * tiles(mean, 256) * tiles(N, 256) > cu_count) return GCFG_256x256;
-  return GCFG_128x128;
+  // tiles of a configuration, and whether they reach `percent` of the CUs
+  auto fills = [&](GroupedCfg c, int64_t percent) {
+    const int64_t t = used == 1 ? tiles(rows, grouped_tile_rows(c)) : rows / grouped_tile_rows(c) + (used + 1) / 2;
+    return 100 * t * tiles(N, grouped_tile_cols(c)) >= percent * cu_count;
+  };
+  // few rows per group: the weights' stream is the work, and narrow tiles
+  // whose waves split K keep most of it in flight (int8, 8 tokens over 64
+  // experts of 2048 x 2048: 22.9 against 25.4 us on 64 x 64 tiles; MXFP4,
+  // 16 rows of 14336 x 4096: 8.9 against 10.3).  With several groups up to 12
+  // rows each (64 groups of 16 rows: int8 51.7 on 64 x 64 tiles against 65.7);
+  // MXFP4, half the bytes per row, up to 6 (8 rows: 31.4 against 34.8);
+  // binary16, twice as many, up to 16 (16 rows: 103 against 104 and more).
+  const bool few = used == 1 ? mean <= 16 : mean <= (kind == KIND_MXFP4 ? 6 : kind == KIND_F16 ? 16 : 12);
+  if (!few) {
+    // 256 x 256 tiles move the fewest bytes per product, but leave a ragged
+    // group's last tile emptier (MXFP4 4096 x 4096 x 4096: 46.5 us against
+    // 53.5 on 128 x 128; 8 groups of 512 rows, N = 14336: 227 against 231, at
+    // N = 4096 59.5 against 44.4)
+    if (used == 1 ? fills(GCFG_256x256, 60) : mean >= 256 && fills(GCFG_256x256, 250)) return GCFG_256x256;
+    // two workgroups of 128 x 128 tiles share a CU: one's stores and first
+    // loads behind the other's products (MXFP4 2048 x 4096 x 4096 28.1 against
+    // 34.8 on 64 x 128; 64 groups of 64 rows 52.0 against 53.6)
+    if (mean >= 48 && fills(GCFG_128x128, 125)) return GCFG_128x128;
+    // int8, 64 groups of 64 rows: 73.9 against 79.1 on 128 x 128 tiles; MXFP4
+    // 256 x 14336 x 4096: 19.2 against 20.1
+    if (mean >= 24 && fills(GCFG_64x128, 150)) return GCFG_64x128;
+    // up to two tiles per CU: the deeper ring (MXFP4 512 x 4096 x 14336 34.1
+    // against 37.9); beyond that: more workgroups (8 groups of 64 rows, N =
+    // 4096: 12.9 against 16.3)
+    if (fills(GCFG_64x64_S2, 201)) return GCFG_64x64_S2;
+    if (fills(GCFG_64x64_S4, 60) || used > 1) return GCFG_64x64_S4;
+  }
+  // the lowest tile that keeps the workgroups near one per CU, up to what the
+  // rows need (MXFP4 16 x 4096 x 4096: 8 rows 5.2 us, 16 rows 6.0; 32 rows
+  // there: 8 rows 6.6, 16 rows 5.9; 64 rows: 32 rows 6.6, 16 rows 7.4)
+  if (used == 1 ? mean <= 8 || !fills(GCFG_SKINNY_8, 126) : mean <= (kind == KIND_F16 ? 2 : 4))
+    return fills(GCFG_SKINNY_8, 201) ? GCFG_SKINNY_8 : GCFG_SKINNY_8_DEEP;
+  if (used == 1 ? mean <= 16 || !fills(GCFG_SKINNY_16, 126) : mean <= 8 || kind != KIND_F16) return GCFG_SKINNY_16;
+  return GCFG_SKINNY_32;
 }
 
 template <int KIND>
@@ -56,18 +96,21 @@ lpgemm_status run_grouped(GroupedArgs p, int cu_count, hipStream_t stream);
 #ifdef LPGEMM_GROUPED_DEFINE
 template <int KIND>
 lpgemm_status run_grouped(GroupedArgs p, int cu_count, hipStream_t stream) {
-  const GroupedCfg cfg = choose_grouped(p.rows, p.groups, p.N, cu_count);
+  const GroupedCfg cfg = choose_grouped(KIND, p.rows, p.groups, p.N, cu_count);
   p.k_stages = (p.row_bytes + 127) / 128;
   p.tiles_n = tiles(p.N, grouped_tile_cols(cfg));
   const int64_t grid = grouped_max_tiles(p.rows, p.groups, grouped_tile_rows(cfg)) * p.tiles_n;
   if (grid > INT32_MAX) return LPGEMM_ERROR_UNSUPPORTED_SHAPE;
   const void* fn = nullptr;
   switch (cfg) {
-    case GCFG_SKINNY_8: fn = (const void*)&grouped_skinny<KIND, 4, 4, 1>; break;
-    case GCFG_SKINNY_16: fn = (const void*)&grouped_skinny<KIND, 4, 4, 2>; break;
-    case GCFG_SKINNY_32: fn = (const void*)&grouped_skinny<KIND, 4, 4, 4>; break;
-    case GCFG_64x128: fn = (const void*)&grouped_tile<KIND, 64, 128, 2, 2, 4, false>; break;
-    case GCFG_128x128: fn = (const void*)&grouped_tile<KIND, 128, 128, 2, 2, 4, false>; break;
+    case GCFG_SKINNY_8_DEEP: fn = (const void*)&grouped_skinny<KIND, 4, 3, 1>; break;
+    case GCFG_SKINNY_8: fn = (const void*)&grouped_skinny<KIND, 4, 2, 1>; break;
+    case GCFG_SKINNY_16: fn = (const void*)&grouped_skinny<KIND, 4, 2, 2>; break;
+    case GCFG_SKINNY_32: fn = (const void*)&grouped_skinny<KIND, 4, 2, 4>; break;
+    case GCFG_64x64_S4: fn = (const void*)&grouped_tile<KIND, 64, 64, 2, 2, 4, false>; break;
+    case GCFG_64x64_S2: fn = (const void*)&grouped_tile<KIND, 64, 64, 2, 2, 2, false>; break;
+    case GCFG_64x128: fn = (const void*)&grouped_tile<KIND, 64, 128, 1, 4, 2, false>; break;
+    case GCFG_128x128: fn = (const void*)&grouped_tile<KIND, 128, 128, 2, 2, 2, false>; break;
     default: fn = (const void*)&grouped_tile<KIND, 256, 256, 2, 2, 2, true>; break;
   }
   void* kargs[] = {&p};

@@ -22,9 +22,9 @@ namespace lpgemm {
 
 constexpr int KIND_MXFP4 = 6;   // beside enum Kind: E2M1 codes with E8M0 scales
 
-typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
-typedef _Float16 f16x4_t __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef float f32x8_t __attribute__((ext_vector_type(8)));
 
 struct GroupedArgs {
   const uint8_t* A;          // rows of row_bytes
@@ -51,18 +51,32 @@ struct GroupTile {
   bool none;
 };
 
+// Tile `in_group` of a group of rows [first, end) in tm_count row tiles: bands
+// of 8 row tiles, column tile by column tile.
+template <int BM>
+__device__ __forceinline__ void place_tile(const GroupedArgs& p, int in_group, int tm_count, int first, int end,
+                                           GroupTile& t) {
+  if (in_group < 0) return;
+  const int band = in_group / (8 * p.tiles_n);
+  const int in_band = in_group - band * 8 * p.tiles_n;
+  const int height = min(tm_count - 8 * band, 8);
+  if (height <= 0) return;
+  const int tm = 8 * band + in_band % height;
+  if (tm < 0 || tm >= tm_count) return;
+  t.tn = in_band / height;
+  t.row0 = first + tm * BM;
+  t.row_end = min(end, t.row0 + BM);
+  t.none = false;
+}
+
 // Row tiles of group g, and its first row and end, with the offsets clamped
 // to the rows there are.
 template <int BM>
 __device__ __forceinline__ int group_tiles(const GroupedArgs& p, int g, int& first, int& end) {
   first = end = 0;
   if (g >= p.groups) return 0;
-  if (!p.offsets) {
-    end = p.rows;
-  } else {
-    first = min(max(p.offsets[g], 0), p.rows);
-    end = min(max(p.offsets[g + 1], 0), p.rows);
-  }
+  first = min(max(p.offsets[g], 0), p.rows);
+  end = min(max(p.offsets[g + 1], 0), p.rows);
   return end > first ? (end - first + BM - 1) / BM : 0;
 }
 
@@ -86,6 +100,12 @@ __device__ __forceinline__ GroupTile find_tile(const GroupedArgs& p, int w) {
   GroupTile t;
   t.none = true;
   t.group = t.row0 = t.row_end = t.tn = 0;
+  if (!p.offsets) {   // one group of all rows
+    const int count = (p.rows + BM - 1) / BM;
+    if (w >= count * p.tiles_n) return t;
+    place_tile<BM>(p, xcd_logical(w, count * p.tiles_n), count, 0, p.rows, t);
+    return t;
+  }
   int first = 0, end = 0;
   int mine = group_tiles<BM>(p, lane, first, end);
   int upto = wave_inclusive_sum(mine);
@@ -111,17 +131,9 @@ __device__ __forceinline__ GroupTile find_tile(const GroupedArgs& p, int w) {
       const int tiles_before = before + __builtin_amdgcn_readlane(upto, l) - tm_count;
       const int gfirst = __builtin_amdgcn_readlane(first, l);
       const int gend = __builtin_amdgcn_readlane(end, l);
-      const int in_group = logical - tiles_before * p.tiles_n;
-      const int band = in_group / (8 * p.tiles_n);
-      const int in_band = in_group - band * 8 * p.tiles_n;
-      const int height = min(tm_count - 8 * band, 8);
-      const int tm = 8 * band + in_band % height;
-      if (tm < 0 || tm >= tm_count) return t;   // counts of overlapping groups may wrap
-      t.tn = in_band / height;
+      // (counts of overlapping groups may wrap: place_tile checks)
+      place_tile<BM>(p, logical - tiles_before * p.tiles_n, tm_count, gfirst, gend, t);
       t.group = g0 + l;
-      t.row0 = gfirst + tm * BM;
-      t.row_end = min(gend, t.row0 + BM);
-      t.none = false;
       return t;
     }
     before += __builtin_amdgcn_readlane(upto, 63);
@@ -172,14 +184,17 @@ __device__ __forceinline__ int scale_mask(int s, int h, int blocks) {
   return left >= 4 ? -1 : (left <= 0 ? 0 : (int)((1u << (8 * left)) - 1));
 }
 
-// binary32 results of four consecutive columns to C's type
-__device__ __forceinline__ void store4(const GroupedArgs& p, size_t idx, const f32x4_t& v) {
-  if (p.out_type == 0) {
-    *(f32x4_t*)(p.C + 4 * idx) = v;
-  } else if (p.out_type == 1) {
-    *(f16x4_t*)(p.C + 2 * idx) = __builtin_convertvector(v, f16x4_t);
+// Consecutive columns' binary32 results as 16 bytes of C: 4 in binary32, 8 in
+// a 16-bit type.  C is not read again: the stores are non-temporal.
+template <int COLS>
+__device__ __forceinline__ void store16(const GroupedArgs& p, size_t idx, const float (&v)[COLS]) {
+  if constexpr (COLS == 4) {
+    __builtin_nontemporal_store(f32x4_t{v[0], v[1], v[2], v[3]}, (f32x4_t*)(p.C + 4 * idx));
   } else {
-    *(bf16x4_t*)(p.C + 2 * idx) = __builtin_convertvector(v, bf16x4_t);
+    const f32x8_t w = {v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7]};
+    const i32x4 h = p.out_type == 1 ? __builtin_bit_cast(i32x4, __builtin_convertvector(w, f16x8))
+                                    : __builtin_bit_cast(i32x4, __builtin_convertvector(w, bf16x8_t));
+    __builtin_nontemporal_store(h, (i32x4*)(p.C + 2 * idx));
   }
 }
 __device__ __forceinline__ void store1(const GroupedArgs& p, size_t idx, float v) {
@@ -199,10 +214,11 @@ __device__ __forceinline__ void store1(const GroupedArgs& p, size_t idx, float v
 // consecutive MXFP4 blocks per stage: one 32-bit word of scale bytes, of
 // which step kk uses byte kk.
 //
-// MXFP4 scales travel with the operands: every second stage one 16-byte load
-// per operand row fetches the scales of two stages (16 blocks) into a ring of
-// their own.  STAGES is even, so that the number of loads a wait may leave in
-// flight is the same in every stage.
+// MXFP4 scales travel with the operands: every fourth stage two 16-byte loads
+// per operand row fetch the scales of four stages (32 blocks, 32 bytes) into
+// one of two buffers of their own.  (A row's scales lie in one cache line per
+// 4096 values of k, which every fetch moves again: 16 bytes per fetch took
+// 8192^3 from 273 us without scales to 307.)
 //
 // PIN: the next stage's loads all go out in the first two K-steps, one MFMA
 // pinned in front of each (the schedule would otherwise issue them back to
@@ -220,20 +236,21 @@ __global__ __launch_bounds__(256) void grouped_tile(GroupedArgs p) {
   static_assert(kRows % 32 == 0 && BM % 32 == 0, "loads per wave");
   constexpr int kSlots = kRows / 32;          // 1 KiB loads per wave per stage (8 rows each)
   constexpr int kSlotsA = BM / 32;
-  constexpr int kSc = MX ? (kRows + 255) / 256 : 0;   // scale loads per wave, every second stage
+  constexpr int kSc = MX ? (kRows / 32 + 3) / 4 : 0;   // scale loads per wave, every fourth stage (32 rows each)
   constexpr int kScBuf = kSc * 4096;
-  constexpr int kScBufs = STAGES / 2 + 1;
-  static_assert(!MX || STAGES % 2 == 0, "scales come every second stage");
-  constexpr int kMainLds = STAGES * kStage + (MX ? kScBufs * kScBuf : 0);
+  // (two buffers: the one filled during stage 4 e + 5 - STAGES was last read
+  // at the end of stage 4 e - 2)
+  static_assert(!MX || (STAGES >= 2 && STAGES <= 6), "scale buffers");
+  constexpr int kMainLds = STAGES * kStage + 2 * kScBuf;
   constexpr int kEpiPitch = WTN * 4 + 32;
   constexpr int kEpiRows = WTM < 64 ? WTM : 64;
   constexpr int kEpiWave = kEpiRows * kEpiPitch;
   constexpr int kLds = kMainLds > 4 * kEpiWave ? kMainLds : 4 * kEpiWave;
   static_assert(kLds <= 160 * 1024, "LDS");
   // loads that may be in flight once stage s + 1 has landed: those of stages
-  // s + 2 .. s + STAGES - 1, (STAGES - 2) / 2 of them with scales
-  constexpr int kInFlight = (STAGES - 2) * kSlots + (STAGES - 2) / 2 * kSc;
-  static_assert(kInFlight <= 63, "vmcnt range");
+  // s + 2 .. s + STAGES - 1, and the scales' where one of them is a fourth
+  constexpr int kInFlight = (STAGES - 2) * kSlots;
+  static_assert(kInFlight + 2 * kSc <= 63, "vmcnt range");
 
   __shared__ __attribute__((aligned(1024))) uint8_t smem[kLds];
 
@@ -277,14 +294,15 @@ __global__ __launch_bounds__(256) void grouped_tile(GroupedArgs p) {
       slot_off[t] = r < 0 ? kOutOfRange : (uint32_t)r * (uint32_t)p.row_bytes + slot_col;
     }
   }
-  // scale slot t of this wave: rows 64 (4 t + wave) + lane
+  // scale slot t of this wave: rows 32 (4 t + wave) + lane / 2, 16 of the 32
+  // bytes
   uint32_t sc_off[MX ? kSc : 1];
   if constexpr (MX) {
 #pragma unroll
     for (int t = 0; t < kSc; ++t) {
-      const int r = 64 * (4 * t + wave) + lane;
+      const int r = 32 * (4 * t + wave) + lane / 2;
       const int src = r < kRows ? source_row(r) : -1;
-      sc_off[t] = src < 0 ? kOutOfRange : (uint32_t)src * (uint32_t)p.scale_stride;
+      sc_off[t] = src < 0 ? kOutOfRange : (uint32_t)src * (uint32_t)p.scale_stride + (lane & 1) * 16;
     }
   }
   auto issue_load = [&](int t, int s) {
@@ -294,20 +312,28 @@ __global__ __launch_bounds__(256) void grouped_tile(GroupedArgs p) {
     if (t < kSlotsA) lds_dma_16(rsrc_a, to, off);
     else lds_dma_16(rsrc_b, to, off);
   };
-  auto issue_scales = [&](int s) {   // s even: blocks 8 s .. 8 s + 15 of every row
+  auto issue_scales = [&](int s) {   // s a multiple of 4: blocks 8 s .. 8 s + 31 of every row
     if constexpr (MX) {
+      const bool inside = 8 * s + (lane & 1) * 16 < p.scale_stride;
 #pragma unroll
       for (int t = 0; t < kSc; ++t) {
-        const uint32_t off = 8 * s < p.scale_stride ? sc_off[t] + 8 * s : kOutOfRange;
-        const uint32_t to = smem_lds + STAGES * kStage + ((s / 2) % kScBufs) * kScBuf + (4 * t + wave) * 1024;
-        // 64 consecutive rows are A's or B's (BM a multiple of 64), or
-        // beyond both
-        if (64 * (4 * t + wave) < BM) lds_dma_16(rsrc_as, to, off);
+        const uint32_t off = inside ? sc_off[t] + 8 * s : kOutOfRange;
+        const uint32_t to = smem_lds + STAGES * kStage + ((s / 4) & 1) * kScBuf + (4 * t + wave) * 1024;
+        if (32 * (4 * t + wave) < BM) lds_dma_16(rsrc_as, to, off);
         else lds_dma_16(rsrc_bs, to, off);
       }
     }
   };
-  static_assert(!MX || BM % 64 == 0, "scale loads take 64 rows of one operand");
+  // own loads of stage s + 1 have landed
+  auto wait_stage = [&](int s) {
+    if constexpr (MX && STAGES > 2) {
+      // is one of stages s + 2 .. s + STAGES - 1 a fourth (with scales)?
+      if (((s + 1) & 3) + STAGES - 2 >= 4) wait_vmcnt<kInFlight + kSc>();
+      else wait_vmcnt<kInFlight>();
+    } else {
+      wait_vmcnt<kInFlight>();
+    }
+  };
 
   const int fr = lane & 31, fh = lane >> 5;
   const int a_base = wm * WTM * 128, b_base = (BM + wn * WTN) * 128;
@@ -323,12 +349,12 @@ __global__ __launch_bounds__(256) void grouped_tile(GroupedArgs p) {
   int sa[TM] = {}, sb[TN] = {}, sa_next[TM] = {}, sb_next[TN] = {};
   auto read_scales = [&](int s) {   // of stage s, into sa_next / sb_next
     if constexpr (MX) {
-      const uint8_t* base = smem + STAGES * kStage + ((s / 2) % kScBufs) * kScBuf + (s & 1) * 8 + fh * 4 + fr * 16;
+      const uint8_t* base = smem + STAGES * kStage + ((s / 4) & 1) * kScBuf + (s & 3) * 8 + fh * 4 + fr * 32;
       const int mask = scale_mask(s, fh, blocks);
 #pragma unroll
-      for (int i = 0; i < TM; ++i) sa_next[i] = *(const int*)(base + (wm * WTM + i * 32) * 16) & mask;
+      for (int i = 0; i < TM; ++i) sa_next[i] = *(const int*)(base + (wm * WTM + i * 32) * 32) & mask;
 #pragma unroll
-      for (int j = 0; j < TN; ++j) sb_next[j] = *(const int*)(base + (BM + wn * WTN + j * 32) * 16) & mask;
+      for (int j = 0; j < TN; ++j) sb_next[j] = *(const int*)(base + (BM + wn * WTN + j * 32) * 32) & mask;
     }
   };
 
@@ -368,13 +394,11 @@ __global__ __launch_bounds__(256) void grouped_tile(GroupedArgs p) {
   if (nks > 0) {
 #pragma unroll
     for (int s = 0; s < STAGES - 1; ++s) {
-      if (s % 2 == 0) issue_scales(s);
+      if (s % 4 == 0) issue_scales(s);
 #pragma unroll
       for (int t = 0; t < kSlots; ++t) issue_load(t, s);
     }
-    // stage 0 has landed; stages 1 .. STAGES - 2 may be in flight (with the
-    // scales of stages 2, 4, ..: (STAGES - 2) / 2 loads, as STAGES is even)
-    wait_vmcnt<kInFlight>();
+    wait_stage(-1);
     block_barrier();
     read_frags(0, 0, 0);
     read_scales(0);
@@ -391,7 +415,7 @@ __global__ __launch_bounds__(256) void grouped_tile(GroupedArgs p) {
       constexpr int src = kk & 1, dst = src ^ 1;
       int nl = 0, pre = 0;
       if constexpr (kk == 0) {
-        if (MX && (sl & 1) == 0) issue_scales(sl);
+        if (MX && (sl & 3) == 0) issue_scales(sl);
       }
       if constexpr (kk < kLoadSteps) {
 #pragma unroll
@@ -419,7 +443,7 @@ __global__ __launch_bounds__(256) void grouped_tile(GroupedArgs p) {
         compute(kk_c, src, 0, kSplit);
         interleave(kSplit, 0, 0);
         __builtin_amdgcn_sched_barrier(0);
-        wait_vmcnt<kInFlight>();   // own loads of stage s + 1 landed
+        wait_stage(s);             // own loads of stage s + 1 landed
         wait_lgkmcnt0();           // own reads of stage s done
         block_barrier();           // ... everyone's
         read_frags(s + 1, 0, dst);
@@ -442,19 +466,8 @@ __global__ __launch_bounds__(256) void grouped_tile(GroupedArgs p) {
   wait_lgkmcnt0();
   block_barrier();
   uint8_t* const stage_out = smem + wave * kEpiWave;
-  constexpr int kLanesPerRow = WTN / 4;
-  constexpr int kRowsPerStore = 64 / kLanesPerRow;
-  static_assert(64 % kLanesPerRow == 0, "whole rows per store");
   const int row0 = tile.row0 + wm * WTM;
-  const int col0 = n0 + wn * WTN + (lane % kLanesPerRow) * 4;
-  const int lane_row = lane / kLanesPerRow;
-  const bool whole = col0 + 4 <= p.N && (p.N & 3) == 0;
-  f32x4_t cs = {0.f, 0.f, 0.f, 0.f};
-  if constexpr (KIND == KIND_I8_DEQUANT) {
-#pragma unroll
-    for (int x = 0; x < 4; ++x)
-      if (col0 + x < p.N) cs[x] = p.col_scale[(size_t)tile.group * p.N + col0 + x];
-  }
+  const int wcol0 = n0 + wn * WTN;
 #pragma unroll
   for (int pass = 0; pass < WTM / kEpiRows; ++pass) {
 #pragma unroll
@@ -477,29 +490,54 @@ __global__ __launch_bounds__(256) void grouped_tile(GroupedArgs p) {
         if (r >= 0) rs_lane = p.row_scale[r];
       }
     }
-    for (int r0 = 0; r0 < kEpiRows; r0 += kRowsPerStore) {
-      const int r = r0 + lane_row;
-      const i32x4 raw = *(const i32x4*)(stage_out + r * kEpiPitch + (lane % kLanesPerRow) * 16);
-      f32x4_t v;
+    // the staged rows, COLS consecutive columns per lane (16 bytes of C: 4 of
+    // binary32, 8 of a 16-bit type)
+    auto store_rows = [&](auto cols_c) __attribute__((always_inline)) {
+      constexpr int COLS = decltype(cols_c)::value;
+      constexpr int kLanesPerRow = WTN / COLS;
+      constexpr int kRowsPerStore = 64 / kLanesPerRow;
+      const int c = (lane % kLanesPerRow) * COLS, col0 = wcol0 + c;
+      const bool whole = col0 + COLS <= p.N && p.N % COLS == 0;
+      float cs[COLS] = {};
       if constexpr (KIND == KIND_I8_DEQUANT) {
-        const float rs = __shfl(rs_lane, r);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) v[x] = ((float)raw[x] * rs) * cs[x];
-      } else {
-        v = __builtin_bit_cast(f32x4_t, raw);
+        for (int x = 0; x < COLS; ++x)
+          if (col0 + x < p.N) cs[x] = p.col_scale[(size_t)tile.group * p.N + col0 + x];
       }
-      const int row = row0 + pass * kEpiRows + r;
-      if (row < tile.row_end) {
-        const size_t idx = (size_t)row * p.N + col0;
-        if (whole) {
-          store4(p, idx, v);
-        } else {
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            if (col0 + x < p.N) store1(p, idx + x, v[x]);
+      for (int r0 = 0; r0 < kEpiRows; r0 += kRowsPerStore) {
+        const int r = r0 + lane / kLanesPerRow;
+        float v[COLS];
+#pragma unroll
+        for (int q = 0; q < COLS / 4; ++q) {
+          const i32x4 raw = *(const i32x4*)(stage_out + r * kEpiPitch + (c + 4 * q) * 4);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int bits = raw[x];
+            if constexpr (KIND == KIND_I8_DEQUANT) v[4 * q + x] = (float)bits;
+            else v[4 * q + x] = __builtin_bit_cast(float, bits);
+          }
+        }
+        if constexpr (KIND == KIND_I8_DEQUANT) {
+          const float rs = __shfl(rs_lane, r);
+#pragma unroll
+          for (int x = 0; x < COLS; ++x) v[x] = (v[x] * rs) * cs[x];
+        }
+        const int row = row0 + pass * kEpiRows + r;
+        if (row < tile.row_end) {
+          const size_t idx = (size_t)row * p.N + col0;
+          if (whole) {
+            store16<COLS>(p, idx, v);
+          } else {
+#pragma unroll
+            for (int x = 0; x < COLS; ++x)
+              if (col0 + x < p.N) store1(p, idx + x, v[x]);
+          }
         }
       }
-    }
+    };
+    if (p.out_type == 0) store_rows(std::integral_constant<int, 4>());
+    else store_rows(std::integral_constant<int, 8>());
     wait_lgkmcnt0();   // reads done before the next pass overwrites them
   }
 }
