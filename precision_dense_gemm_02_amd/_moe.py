@@ -22,6 +22,8 @@ MAX_K_MXFP4 = 1048576
 
 _TYPE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 _HALF = {torch.float16: 1, torch.bfloat16: 2}
+_Tensor, _empty = torch.Tensor, torch.empty
+_F32, _I32, _I8, _U8 = torch.float32, torch.int32, torch.int8, torch.uint8
 
 _SIGNATURES = {
     "lpgemm_add_rmsnorm_quantize": [_i64, _i64, _int, _p, _i64, _p, _i64, _p, _f32, _p, _i64, _p, _p, _p],
@@ -46,56 +48,85 @@ def _function(name: str):
     return f
 
 
+def _stream_of(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# torch's own accessor of the current stream's handle, without a Stream object
+_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _stream_of)
+
+
 def _call(name: str, dev, *args) -> None:
     """The entry point `name` on the current stream of `dev`."""
     f = _functions.get(name) or _function(name)
     index = dev.index
     if index == torch.cuda.current_device():
-        status = f(*args, torch.cuda.current_stream(dev).cuda_stream)
+        status = f(*args, _stream(index))
     else:
         with torch.cuda.device(dev):
-            status = f(*args, torch.cuda.current_stream(dev).cuda_stream)
+            status = f(*args, _stream(index))
     if status:
         raise LpgemmError(status, name)
 
 
-def _tensor(t, name, dtypes, dims):
-    if not isinstance(t, torch.Tensor):
+def _refuse(t, name, dtypes, shape=None, dev=None, dims=None):
+    """Says what is wrong with a tensor that failed a check."""
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    if t.dim() != dims:
+    if dims is not None and t.dim() != dims:
         raise ValueError(f"{name} must be {dims}-D, got shape {tuple(t.shape)}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a GPU device")
+    if dev is not None and t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, as the other tensors are")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _full(t, name, dtypes, shape, dev):
-    """A contiguous tensor of that shape."""
-    _tensor(t, name, dtypes, len(shape))
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+def _full(t, name, dtype, shape, dev):
+    """A contiguous tensor of that type and shape on `dev`."""
+    if not isinstance(t, _Tensor) or t.dtype is not dtype or t.shape != shape or t.device != dev \
+            or not t.is_contiguous():
+        _refuse(t, name, (dtype,), shape, dev)
+
+
+def _operand(t, name, dtype, dims):
+    """A contiguous GPU tensor of that type."""
+    if not isinstance(t, _Tensor) or t.dtype is not dtype or t.dim() != dims or not t.is_cuda \
+            or not t.is_contiguous():
+        _refuse(t, name, (dtype,), dims=dims)
 
 
 def _rows(t, name, dtypes):
-    """A matrix whose rows are contiguous; returns its row stride (a stride
-    that no element uses counts as the row's length)."""
-    _tensor(t, name, dtypes, 2)
+    """A matrix whose rows are contiguous: (rows, columns, row stride), the
+    stride being the row's length where no element uses it."""
+    if not isinstance(t, _Tensor) or t.dtype not in dtypes or t.dim() != 2 or not t.is_cuda:
+        _refuse(t, name, dtypes, dims=2)
     M, K = t.shape
-    if K > 1 and t.stride(1) != 1:
+    if M <= 1 or K == 0:
+        return M, K, K
+    stride, along = t.stride()
+    if along != 1 and K > 1:
         raise ValueError(f"the rows of {name} must be contiguous")
-    return t.stride(0) if M > 1 and K else K
+    return M, K, stride
 
 
 def _out(out, name, shape, dtype, dev):
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    _full(out, name, (dtype,), torch.Size(shape), dev)
+        return _empty(shape, dtype=dtype, device=dev)
+    _full(out, name, dtype, shape, dev)
     return out
+
+
+def _row_stride(t, name, x):
+    """The row stride of a matrix that must go with x."""
+    M, K, stride = _rows(t, name, (x.dtype,))
+    if t.shape != x.shape or t.device != x.device:
+        raise ValueError(f"{name} must have x's shape {tuple(x.shape)} and be on {x.device}")
+    return stride
 
 
 def add_rmsnorm_quantize(x, weight, eps: float, residual=None, residual_out=None, q_out=None, scale_out=None):
@@ -107,26 +138,22 @@ def add_rmsnorm_quantize(x, weight, eps: float, residual=None, residual_out=None
     stride is a multiple of 8; weight: K values of the same type.  h goes to
     `residual_out` (M x K, may be x or residual itself) or a new tensor.  A
     row with a non-finite value gets scale NaN and codes 0."""
-    stride = _rows(x, "x", _HALF)
-    M, K = x.shape
+    M, K, stride = _rows(x, "x", _HALF)
     dev, dtype = x.device, x.dtype
-    _full(weight, "weight", (dtype,), torch.Size((K,)), dev)
-    h, r_ptr, r_stride, h_ptr, h_stride = x, None, 0, None, 0
+    _full(weight, "weight", dtype, (K,), dev)
+    h, r_ptr, r_stride, h_ptr, h_stride = residual_out, None, 0, None, 0
     if residual is not None:
-        r_stride = _rows(residual, "residual", (dtype,))
-        if residual.shape != x.shape or residual.device != dev:
-            raise ValueError(f"residual must have x's shape {(M, K)} and device")
+        r_stride = _row_stride(residual, "residual", x)
         r_ptr = residual.data_ptr()
-        h = torch.empty((M, K), dtype=dtype, device=dev) if residual_out is None else residual_out
-    elif residual_out is not None:
-        h = residual_out
-    if h is not x or residual is not None:
-        h_stride = _rows(h, "residual_out", (dtype,))
-        if h.shape != x.shape or h.device != dev:
-            raise ValueError(f"residual_out must have x's shape {(M, K)} and device")
+        if h is None:
+            h = _empty((M, K), dtype=dtype, device=dev)
+    if h is None:
+        h = x
+    else:
+        h_stride = _row_stride(h, "residual_out", x)
         h_ptr = h.data_ptr()
-    q = _out(q_out, "q_out", (M, K), torch.int8, dev)
-    scale = _out(scale_out, "scale_out", (M,), torch.float32, dev)
+    q = _out(q_out, "q_out", (M, K), _I8, dev)
+    scale = _out(scale_out, "scale_out", (M,), _F32, dev)
     _call("lpgemm_add_rmsnorm_quantize", dev, M, K, _HALF[dtype], x.data_ptr(), stride, r_ptr, r_stride,
           weight.data_ptr(), eps, h_ptr, h_stride, q.data_ptr(), scale.data_ptr())
     return q, scale, h
@@ -136,13 +163,12 @@ def silu_mul_quantize(x, q_out=None, scale_out=None):
     """silu(gate) * up with int8 rows: x is M x 2K fp16 or bf16, a row's K gate
     values before its K up values (contiguous rows, a row stride that is a
     multiple of 8); returns (q int8 M x K, scale fp32 M)."""
-    stride = _rows(x, "x", _HALF)
-    M, K2 = x.shape
+    M, K2, stride = _rows(x, "x", _HALF)
     if K2 % 2:
         raise ValueError(f"x must have an even number of columns, got {K2}")
     K, dev = K2 // 2, x.device
-    q = _out(q_out, "q_out", (M, K), torch.int8, dev)
-    scale = _out(scale_out, "scale_out", (M,), torch.float32, dev)
+    q = _out(q_out, "q_out", (M, K), _I8, dev)
+    scale = _out(scale_out, "scale_out", (M,), _F32, dev)
     _call("lpgemm_silu_mul_quantize", dev, M, K, _HALF[x.dtype], x.data_ptr(), stride, q.data_ptr(), scale.data_ptr())
     return q, scale
 
@@ -159,25 +185,20 @@ def quantize_mxfp4(x, codes_out=None, scales_out=None):
     with contiguous rows and a row stride that is a multiple of 8; K a
     multiple of 32.  Weights of several experts: quantise them as one matrix
     of groups * N rows and reshape the results."""
-    stride = _rows(x, "x", _HALF)
-    rows, K = x.shape
+    rows, K, stride = _rows(x, "x", _HALF)
     dev = x.device
-    codes = _out(codes_out, "codes_out", (rows, K // 2), torch.uint8, dev)
-    scales = _out(scales_out, "scales_out", (rows, mxfp4_scale_stride(K)), torch.uint8, dev)
+    codes = _out(codes_out, "codes_out", (rows, K // 2), _U8, dev)
+    scales = _out(scales_out, "scales_out", (rows, mxfp4_scale_stride(K)), _U8, dev)
     _call("lpgemm_quantize_mxfp4", dev, rows, K, _HALF[x.dtype], x.data_ptr(), stride, codes.data_ptr(),
           scales.data_ptr())
     return codes, scales
 
 
-_U8 = (torch.uint8,)
-
-
 def _mxfp4_operand(codes, scales, name, dims):
-    _tensor(codes, name, _U8, dims)
-    if not codes.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    K = 2 * codes.shape[-1]
-    _full(scales, name + "_scale", _U8, torch.Size((*codes.shape[:-1], mxfp4_scale_stride(K))), codes.device)
+    _operand(codes, name, _U8, dims)
+    *rows, half = codes.shape
+    K = 2 * half
+    _full(scales, name + "_scale", _U8, (*rows, mxfp4_scale_stride(K)), codes.device)
     return K
 
 
@@ -213,26 +234,22 @@ def gemm_mxfp4(a, a_scale, b, b_scale, out_dtype=torch.float32, out=None):
     return out
 
 
-_I32 = (torch.int32,)
-
-
 def _routing(a, b, offsets, row_index):
-    """Checks the groups of a product: (rows of C, rows of a, groups, N)."""
+    """Checks the groups of a product (a and b are checked on their own):
+    (rows of C, rows of a, groups, N, row_index's address)."""
     dev = a.device
     groups, N, width = b.shape
-    if a.shape[1] != width:
-        raise ValueError(f"K mismatch: a {tuple(a.shape)}, b_t {tuple(b.shape)}")
-    if not a.is_contiguous() or not b.is_contiguous():
-        raise ValueError("a and b_t must be contiguous")
+    a_rows, own = a.shape
+    if own != width:
+        raise ValueError(f"K mismatch: a {tuple(a.shape)}, b {tuple(b.shape)}")
     if b.device != dev:
         raise ValueError("all tensors must be on the same device")
-    _full(offsets, "offsets", _I32, torch.Size((groups + 1,)), dev)
-    a_rows = a.shape[0]
+    _full(offsets, "offsets", _I32, (groups + 1,), dev)
     if row_index is None:
         return a_rows, a_rows, groups, N, None
-    _tensor(row_index, "row_index", _I32, 1)
-    if row_index.device != dev or not row_index.is_contiguous():
-        raise ValueError(f"row_index must be a contiguous vector on {dev}")
+    _operand(row_index, "row_index", _I32, 1)
+    if row_index.device != dev:
+        raise ValueError("all tensors must be on the same device")
     return row_index.shape[0], a_rows, groups, N, row_index.data_ptr()
 
 
@@ -246,12 +263,12 @@ def gemm_i8_dequant_grouped(a, b_t, offsets, row_scale, col_scale, row_index: Op
     row_index: int32, one per row of C (None: row i is a's row i); row_scale:
     fp32, one per row of a; col_scale: groups x N fp32.  offsets and row_index
     are read on the device.  Rows outside every group are not written."""
-    _tensor(a, "a", (torch.int8,), 2)
-    _tensor(b_t, "b_t", (torch.int8,), 3)
+    _operand(a, "a", _I8, 2)
+    _operand(b_t, "b_t", _I8, 3)
     rows, a_rows, groups, N, index = _routing(a, b_t, offsets, row_index)
     dev = a.device
-    _full(row_scale, "row_scale", (torch.float32,), torch.Size((a_rows,)), dev)
-    _full(col_scale, "col_scale", (torch.float32,), torch.Size((groups, N)), dev)
+    _full(row_scale, "row_scale", _F32, (a_rows,), dev)
+    _full(col_scale, "col_scale", _F32, (groups, N), dev)
     out = _out(out, "out", (rows, N), _out_dtype(out_dtype), dev)
     _call("lpgemm_i8_dequant_grouped", dev, rows, groups, N, a.shape[1], a_rows, a.data_ptr(), b_t.data_ptr(),
           offsets.data_ptr(), index, row_scale.data_ptr(), col_scale.data_ptr(), _TYPE[out_dtype], out.data_ptr())
@@ -261,8 +278,8 @@ def gemm_i8_dequant_grouped(a, b_t, offsets, row_scale, col_scale, row_index: Op
 def gemm_f16_grouped(a, b_t, offsets, row_index: Optional[torch.Tensor] = None, out_dtype=torch.float32, out=None):
     """gemm_i8_dequant_grouped for fp16 operands, summed in fp32, without
     scales: C[i] = a[row_index[i]] . b_t[g]."""
-    _tensor(a, "a", (torch.float16,), 2)
-    _tensor(b_t, "b_t", (torch.float16,), 3)
+    _operand(a, "a", torch.float16, 2)
+    _operand(b_t, "b_t", torch.float16, 3)
     rows, a_rows, groups, N, index = _routing(a, b_t, offsets, row_index)
     dev = a.device
     out = _out(out, "out", (rows, N), _out_dtype(out_dtype), dev)
