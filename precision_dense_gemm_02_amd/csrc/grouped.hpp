@@ -107,11 +107,11 @@ lpgemm_status run_grouped(GroupedArgs p, int cu_count, hipStream_t stream) {
     case GCFG_SKINNY_8: fn = (const void*)&grouped_skinny<KIND, 4, 2, 1>; break;
     case GCFG_SKINNY_16: fn = (const void*)&grouped_skinny<KIND, 4, 2, 2>; break;
     case GCFG_SKINNY_32: fn = (const void*)&grouped_skinny<KIND, 4, 2, 4>; break;
-    case GCFG_64x64_S4: fn = (const void*)&grouped_tile<KIND, 64, 64, 2, 2, 4, false>; break;
-    case GCFG_64x64_S2: fn = (const void*)&grouped_tile<KIND, 64, 64, 2, 2, 2, false>; break;
-    case GCFG_64x128: fn = (const void*)&grouped_tile<KIND, 64, 128, 1, 4, 2, false>; break;
-    case GCFG_128x128: fn = (const void*)&grouped_tile<KIND, 128, 128, 2, 2, 2, false>; break;
-    default: fn = (const void*)&grouped_tile<KIND, 256, 256, 2, 2, 2, true>; break;
+    case GCFG_64x64_S4: fn = (const void*)&grouped_tile<KIND, 64, 64, 2, 2, 4, false, false>; break;
+    case GCFG_64x64_S2: fn = (const void*)&grouped_tile<KIND, 64, 64, 2, 2, 2, false, false>; break;
+    case GCFG_64x128: fn = (const void*)&grouped_tile<KIND, 64, 128, 1, 4, 2, false, false>; break;
+    case GCFG_128x128: fn = (const void*)&grouped_tile<KIND, 128, 128, 2, 2, 2, false, true>; break;
+    default: fn = (const void*)&grouped_tile<KIND, 256, 256, 2, 2, 2, true, true>; break;
   }
   void* kargs[] = {&p};
   return hipLaunchKernel(fn, dim3((unsigned)grid), dim3(256), kargs, 0, stream) == hipSuccess ? LPGEMM_SUCCESS

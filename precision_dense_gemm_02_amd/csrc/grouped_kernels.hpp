@@ -223,7 +223,13 @@ __device__ __forceinline__ void store1(const GroupedArgs& p, size_t idx, float v
 // PIN: the next stage's loads all go out in the first two K-steps, one MFMA
 // pinned in front of each (the schedule would otherwise issue them back to
 // back); without it they are spread over the first three K-steps.
-template <int KIND, int BM, int BN, int WM, int WN, int STAGES, bool PIN>
+//
+// TAIL: a group's last tile runs the main loop for the 32-row blocks that its
+// rows reach, in steps of WM blocks; its loads and products for the other
+// rows are left out.  There the waves' rows alternate by block, so that the
+// blocks fall on all of them; in a whole tile each wave has one run of rows
+// (alternating there too took 8192^3 from 272 to 279 us).  Needs two stages.
+template <int KIND, int BM, int BN, int WM, int WN, int STAGES, bool PIN, bool TAIL>
 __global__ __launch_bounds__(256) void grouped_tile(GroupedArgs p) {
   using Acc = typename GroupedAcc<KIND>::type;
   using Layout = RowLayout<128>;
@@ -241,6 +247,7 @@ __global__ __launch_bounds__(256) void grouped_tile(GroupedArgs p) {
   // (two buffers: the one filled during stage 4 e + 5 - STAGES was last read
   // at the end of stage 4 e - 2)
   static_assert(!MX || (STAGES >= 2 && STAGES <= 6), "scale buffers");
+  static_assert(!TAIL || STAGES == 2, "fewer loads in flight than the waits of a longer ring count");
   constexpr int kMainLds = STAGES * kStage + 2 * kScBuf;
   constexpr int kEpiPitch = WTN * 4 + 32;
   constexpr int kEpiRows = WTM < 64 ? WTM : 64;
@@ -294,15 +301,17 @@ __global__ __launch_bounds__(256) void grouped_tile(GroupedArgs p) {
       slot_off[t] = r < 0 ? kOutOfRange : (uint32_t)r * (uint32_t)p.row_bytes + slot_col;
     }
   }
-  // scale slot t of this wave: rows 32 (4 t + wave) + lane / 2, 16 of the 32
-  // bytes
+  // scale slot t of this wave: rows 32 (4 t + wave) + lane / 2, 16 of their 32
+  // bytes; the halves of every second 8 rows change places, so that the words
+  // of 16 consecutive rows lie in different banks
+  const int sc_half = ((lane & 1) ^ ((lane >> 4) & 1)) * 16;
   uint32_t sc_off[MX ? kSc : 1];
   if constexpr (MX) {
 #pragma unroll
     for (int t = 0; t < kSc; ++t) {
       const int r = 32 * (4 * t + wave) + lane / 2;
       const int src = r < kRows ? source_row(r) : -1;
-      sc_off[t] = src < 0 ? kOutOfRange : (uint32_t)src * (uint32_t)p.scale_stride + (lane & 1) * 16;
+      sc_off[t] = src < 0 ? kOutOfRange : (uint32_t)src * (uint32_t)p.scale_stride + sc_half;
     }
   }
   auto issue_load = [&](int t, int s) {
@@ -314,7 +323,7 @@ __global__ __launch_bounds__(256) void grouped_tile(GroupedArgs p) {
   };
   auto issue_scales = [&](int s) {   // s a multiple of 4: blocks 8 s .. 8 s + 31 of every row
     if constexpr (MX) {
-      const bool inside = 8 * s + (lane & 1) * 16 < p.scale_stride;
+      const bool inside = 8 * s + sc_half < p.scale_stride;
 #pragma unroll
       for (int t = 0; t < kSc; ++t) {
         const uint32_t off = inside ? sc_off[t] + 8 * s : kOutOfRange;
@@ -336,28 +345,14 @@ __global__ __launch_bounds__(256) void grouped_tile(GroupedArgs p) {
   };
 
   const int fr = lane & 31, fh = lane >> 5;
-  const int a_base = wm * WTM * 128, b_base = (BM + wn * WTN) * 128;
+  // block i of a wave is the tile's 32-row block step i + base: the wave's own
+  // run of rows, or, in a partial tile, every WM-th block
+  const int used_blocks = TAIL ? (tile.row_end - tile.row0 + 32 * WM - 1) / (32 * WM) : TM;
+  const bool partial = TAIL && used_blocks < TM;
+  const int b_base = (BM + wn * WTN) * 128;
   i32x4 fa[2][TM], fb[2][TN];
-  auto read_frags = [&](int s, int kk, int dst) {
-    const uint8_t* base = smem + (s % STAGES) * kStage + Layout::off(fr, 4 * fh + kk);
-#pragma unroll
-    for (int i = 0; i < TM; ++i) fa[dst][i] = *(const i32x4*)(base + a_base + i * 4096);
-#pragma unroll
-    for (int j = 0; j < TN; ++j) fb[dst][j] = *(const i32x4*)(base + b_base + j * 4096);
-  };
   const int blocks = p.row_bytes / 16;   // MXFP4 blocks of 32 values (16 bytes)
   int sa[TM] = {}, sb[TN] = {}, sa_next[TM] = {}, sb_next[TN] = {};
-  auto read_scales = [&](int s) {   // of stage s, into sa_next / sb_next
-    if constexpr (MX) {
-      const uint8_t* base = smem + STAGES * kStage + ((s / 4) & 1) * kScBuf + (s & 3) * 8 + fh * 4 + fr * 32;
-      const int mask = scale_mask(s, fh, blocks);
-#pragma unroll
-      for (int i = 0; i < TM; ++i) sa_next[i] = *(const int*)(base + (wm * WTM + i * 32) * 32) & mask;
-#pragma unroll
-      for (int j = 0; j < TN; ++j) sb_next[j] = *(const int*)(base + (BM + wn * WTN + j * 32) * 32) & mask;
-    }
-  };
-
   Acc acc[TM][TN];
 #pragma unroll
   for (int i = 0; i < TM; ++i)
@@ -366,96 +361,145 @@ __global__ __launch_bounds__(256) void grouped_tile(GroupedArgs p) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
 
-  constexpr int kMfma = TM * TN;
-  auto compute = [&](auto kk_c, int src, int first, int last) {
-    constexpr int kk = decltype(kk_c)::value;
-#pragma unroll
-    for (int x = 0; x < kMfma; ++x) {
-      if (x < first || x >= last) continue;
-      const int i = x / TN, j = x % TN;
-      acc[i][j] = grouped_mfma<KIND, kk>(fa[src][i], fb[src][j], acc[i][j], sa[i], sb[j]);
-    }
-  };
-  constexpr int kSplit = kMfma > 1 ? kMfma / 2 : 1;
-  constexpr int kReads = TM + TN;
   constexpr int kLoadSteps = PIN ? 2 : 3;
   constexpr int kLoadsPerStep = (kSlots + kLoadSteps - 1) / kLoadSteps;
-  auto interleave = [&](int mfmas, int reads, int loads) {
-#pragma unroll
-    for (int x = 0; x < kMfma; ++x) {
-      if (x >= mfmas) break;
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                  // MFMA
-      if (x < reads) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // DS read
-      if (x < loads) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);   // VMEM read
-    }
-  };
-
   const int nks = p.k_stages;   // 0 when K = 0: C is written as zeros
-  if (nks > 0) {
+
+  // the main loop over the first TMU blocks of every wave
+  auto main_loop = [&](auto tmu_c) __attribute__((always_inline)) {
+    constexpr int TMU = decltype(tmu_c)::value;
+    constexpr int kMfma = TMU * TN;
+    constexpr int kStep = TMU == TM ? 1 : WM;
+    const int row_base = TMU == TM ? wm * TM : wm;
+    const int a_base = row_base * 4096;
+    constexpr int kSplit = kMfma > 1 ? kMfma / 2 : 1;
+    constexpr int kReads = TMU + TN;
+    constexpr int kSlotsUsed = kSlotsA * TMU / TM;   // of A's load slots
+    auto used = [](int t) { return t < kSlotsUsed || t >= kSlotsA; };
+    auto read_frags = [&](int s, int kk, int dst) {
+      const uint8_t* base = smem + (s % STAGES) * kStage + Layout::off(fr, 4 * fh + kk);
 #pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s) {
-      if (s % 4 == 0) issue_scales(s);
+      for (int i = 0; i < TMU; ++i) fa[dst][i] = *(const i32x4*)(base + a_base + kStep * i * 4096);
 #pragma unroll
-      for (int t = 0; t < kSlots; ++t) issue_load(t, s);
-    }
-    wait_stage(-1);
-    block_barrier();
-    read_frags(0, 0, 0);
-    read_scales(0);
-  }
-  for (int s = 0; s < nks; ++s) {
-    // loads for stage s + STAGES - 1 (past the last stage they move no data)
-    const int sl = s + STAGES - 1;
+      for (int j = 0; j < TN; ++j) fb[dst][j] = *(const i32x4*)(base + b_base + j * 4096);
+    };
+    auto read_scales = [&](int s) {   // of stage s, into sa_next / sb_next
+      if constexpr (MX) {
+        const uint8_t* base = smem + STAGES * kStage + ((s / 4) & 1) * kScBuf + fr * 32 +
+                              ((((s >> 1) ^ (fr >> 3)) & 1) << 4) + (s & 1) * 8 + fh * 4;
 #pragma unroll
-    for (int i = 0; i < TM; ++i) sa[i] = sa_next[i];
+        for (int i = 0; i < TMU; ++i) sa_next[i] = *(const int*)(base + (kStep * i + row_base) * 1024);
 #pragma unroll
-    for (int j = 0; j < TN; ++j) sb[j] = sb_next[j];
-    auto step = [&](auto kk_c) __attribute__((always_inline)) {
-      constexpr int kk = decltype(kk_c)::value;
-      constexpr int src = kk & 1, dst = src ^ 1;
-      int nl = 0, pre = 0;
-      if constexpr (kk == 0) {
-        if (MX && (sl & 3) == 0) issue_scales(sl);
-      }
-      if constexpr (kk < kLoadSteps) {
-#pragma unroll
-        for (int t = 0; t < kSlots; ++t) {
-          if (t / kLoadsPerStep != kk) continue;
-          if constexpr (PIN) {
-            if (pre < kMfma) {
-              compute(kk_c, src, pre, pre + 1);
-              ++pre;
-              __builtin_amdgcn_sched_barrier(0);
-            }
-            issue_load(t, sl);
-            __builtin_amdgcn_sched_barrier(0);
-          } else {
-            issue_load(t, sl);
-            ++nl;
-          }
-        }
-      }
-      if constexpr (kk < 3) {
-        read_frags(s, kk + 1, dst);
-        compute(kk_c, src, pre, kMfma);
-        interleave(kMfma - pre, kReads, nl);
-      } else {
-        compute(kk_c, src, 0, kSplit);
-        interleave(kSplit, 0, 0);
-        __builtin_amdgcn_sched_barrier(0);
-        wait_stage(s);             // own loads of stage s + 1 landed
-        wait_lgkmcnt0();           // own reads of stage s done
-        block_barrier();           // ... everyone's
-        read_frags(s + 1, 0, dst);
-        read_scales(s + 1);
-        compute(kk_c, src, kSplit, kMfma);
-        interleave(kMfma - kSplit, kReads, 0);
+        for (int j = 0; j < TN; ++j) sb_next[j] = *(const int*)(base + (BM + wn * WTN + j * 32) * 32);
       }
     };
-    step(std::integral_constant<int, 0>());
-    step(std::integral_constant<int, 1>());
-    step(std::integral_constant<int, 2>());
-    step(std::integral_constant<int, 3>());
+    auto compute = [&](auto kk_c, int src, int first, int last) {
+      constexpr int kk = decltype(kk_c)::value;
+#pragma unroll
+      for (int x = 0; x < kMfma; ++x) {
+        if (x < first || x >= last) continue;
+        const int i = x / TN, j = x % TN;
+        acc[i][j] = grouped_mfma<KIND, kk>(fa[src][i], fb[src][j], acc[i][j], sa[i], sb[j]);
+      }
+    };
+    auto interleave = [&](int mfmas, int reads, int loads) {
+#pragma unroll
+      for (int x = 0; x < kMfma; ++x) {
+        if (x >= mfmas) break;
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                  // MFMA
+        if (x < reads) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // DS read
+        if (x < loads) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);   // VMEM read
+      }
+    };
+    if (nks > 0) {
+#pragma unroll
+      for (int s = 0; s < STAGES - 1; ++s) {
+        if (s % 4 == 0) issue_scales(s);
+#pragma unroll
+        for (int t = 0; t < kSlots; ++t)
+          if (used(t)) issue_load(t, s);
+      }
+      wait_stage(-1);
+      block_barrier();
+      read_frags(0, 0, 0);
+      read_scales(0);
+    }
+    for (int s = 0; s < nks; ++s) {
+      // loads for stage s + STAGES - 1 (past the last stage they move no data)
+      const int sl = s + STAGES - 1;
+      if constexpr (MX) {
+#pragma unroll
+        for (int i = 0; i < TMU; ++i) sa[i] = sa_next[i];
+#pragma unroll
+        for (int j = 0; j < TN; ++j) sb[j] = sb_next[j];
+        if (8 * s + 8 > blocks) {   // the row ends inside the stage: padding bytes follow
+          const int mask = scale_mask(s, fh, blocks);
+#pragma unroll
+          for (int i = 0; i < TMU; ++i) sa[i] &= mask;
+#pragma unroll
+          for (int j = 0; j < TN; ++j) sb[j] &= mask;
+        }
+      }
+      auto step = [&](auto kk_c) __attribute__((always_inline)) {
+        constexpr int kk = decltype(kk_c)::value;
+        constexpr int src = kk & 1, dst = src ^ 1;
+        int nl = 0, pre = 0;
+        if constexpr (kk == 0) {
+          if (MX && (sl & 3) == 0) issue_scales(sl);
+        }
+        if constexpr (kk < kLoadSteps) {
+#pragma unroll
+          for (int t = 0; t < kSlots; ++t) {
+            if (t / kLoadsPerStep != kk || !used(t)) continue;
+            if constexpr (PIN) {
+              if (pre < kMfma) {
+                compute(kk_c, src, pre, pre + 1);
+                ++pre;
+                __builtin_amdgcn_sched_barrier(0);
+              }
+              issue_load(t, sl);
+              __builtin_amdgcn_sched_barrier(0);
+            } else {
+              issue_load(t, sl);
+              ++nl;
+            }
+          }
+        }
+        if constexpr (kk < 3) {
+          read_frags(s, kk + 1, dst);
+          compute(kk_c, src, pre, kMfma);
+          interleave(kMfma - pre, kReads, nl);
+        } else {
+          compute(kk_c, src, 0, kSplit);
+          interleave(kSplit, 0, 0);
+          __builtin_amdgcn_sched_barrier(0);
+          wait_stage(s);             // own loads of stage s + 1 landed
+          wait_lgkmcnt0();           // own reads of stage s done
+          block_barrier();           // ... everyone's
+          read_frags(s + 1, 0, dst);
+          read_scales(s + 1);
+          compute(kk_c, src, kSplit, kMfma);
+          interleave(kMfma - kSplit, kReads, 0);
+        }
+      };
+      step(std::integral_constant<int, 0>());
+      step(std::integral_constant<int, 1>());
+      step(std::integral_constant<int, 2>());
+      step(std::integral_constant<int, 3>());
+    }
+  };
+  if constexpr (TAIL && TM == 4) {
+    switch (used_blocks) {
+      case 1: main_loop(std::integral_constant<int, 1>()); break;
+      case 2: main_loop(std::integral_constant<int, 2>()); break;
+      case 3: main_loop(std::integral_constant<int, 3>()); break;
+      default: main_loop(std::integral_constant<int, 4>()); break;
+    }
+  } else if constexpr (TAIL && TM == 2) {
+    if (used_blocks == 1) main_loop(std::integral_constant<int, 1>());
+    else main_loop(std::integral_constant<int, 2>());
+  } else {
+    main_loop(std::integral_constant<int, TM>());
   }
 
   // Epilogue.  Every outstanding load (all past the last stage) lands before
@@ -466,10 +510,15 @@ __global__ __launch_bounds__(256) void grouped_tile(GroupedArgs p) {
   wait_lgkmcnt0();
   block_barrier();
   uint8_t* const stage_out = smem + wave * kEpiWave;
-  const int row0 = tile.row0 + wm * WTM;
+  // row of C behind row r that this wave stages in a pass
+  auto row_of = [&](int pass, int r) -> int {
+    const int i = pass * (kEpiRows / 32) + r / 32;
+    return tile.row0 + (partial ? i * WM + wm : wm * TM + i) * 32 + r % 32;
+  };
   const int wcol0 = n0 + wn * WTN;
 #pragma unroll
   for (int pass = 0; pass < WTM / kEpiRows; ++pass) {
+    if (pass * (kEpiRows / 32) >= used_blocks) break;
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
@@ -486,7 +535,7 @@ __global__ __launch_bounds__(256) void grouped_tile(GroupedArgs p) {
     float rs_lane = 0.f;
     if constexpr (KIND == KIND_I8_DEQUANT) {
       if (lane < kEpiRows) {
-        const int r = a_row_of(p, row0 + pass * kEpiRows + lane, tile.row_end);
+        const int r = a_row_of(p, row_of(pass, lane), tile.row_end);
         if (r >= 0) rs_lane = p.row_scale[r];
       }
     }
@@ -523,7 +572,7 @@ __global__ __launch_bounds__(256) void grouped_tile(GroupedArgs p) {
 #pragma unroll
           for (int x = 0; x < COLS; ++x) v[x] = (v[x] * rs) * cs[x];
         }
-        const int row = row0 + pass * kEpiRows + r;
+        const int row = row_of(pass, r);
         if (row < tile.row_end) {
           const size_t idx = (size_t)row * p.N + col0;
           if (whole) {
