@@ -41,7 +41,8 @@ inline int64_t grouped_max_tiles(int64_t rows, int64_t groups, int tile) {
 
 // The kernel for the sizes.  How the rows fall on the groups is known on the
 // device only; the choice goes by the mean, and by how many tiles the rows
-// would make if half the groups ended in a tile of their own.  Measured at
+// would make if half the groups ended in a tile of their own (and most had
+// one).  Measured at
 // 250 sizes of one group (1 to 4096 rows) and of 8 to 128 groups (1 to 2048
 // tokens, 2 or 8 experts each), N = 768 to 14336, K = 2048 to 14336 (graph
 // replay, one MI355X; the figures at each rule are us with the kernel it
@@ -51,7 +52,8 @@ inline GroupedCfg choose_grouped(int kind, int64_t rows, int64_t groups, int64_t
   const int64_t mean = (rows + used - 1) / used;
   // tiles of a configuration, and whether they reach `percent` of the CUs
   auto fills = [&](GroupedCfg c, int64_t percent) {
-    const int64_t t = used == 1 ? tiles(rows, grouped_tile_rows(c)) : rows / grouped_tile_rows(c) + (used + 1) / 2;
+    const int64_t ragged = rows / grouped_tile_rows(c) + (used + 1) / 2, most = (4 * used + 4) / 5;
+    const int64_t t = used == 1 ? tiles(rows, grouped_tile_rows(c)) : ragged > most ? ragged : most;
     return 100 * t * tiles(N, grouped_tile_cols(c)) >= percent * cu_count;
   };
   // few rows per group: the weights' stream is the work, and narrow tiles
@@ -70,24 +72,48 @@ inline GroupedCfg choose_grouped(int kind, int64_t rows, int64_t groups, int64_t
     if (used == 1 ? fills(GCFG_256x256, 60) : mean >= 256 && fills(GCFG_256x256, 250)) return GCFG_256x256;
     // two workgroups of 128 x 128 tiles share a CU: one's stores and first
     // loads behind the other's products (MXFP4 2048 x 4096 x 4096 28.1 against
-    // 34.8 on 64 x 128; 64 groups of 64 rows 52.0 against 53.6)
-    if (mean >= 48 && fills(GCFG_128x128, 125)) return GCFG_128x128;
+    // 34.8 on 64 x 128; 3000 x 1536 x 3584 18.7 against 25.5; 1024 x 4096 x
+    // 4096, one tile per CU, 20.6 against 19.4)
+    if (mean >= 48 && fills(GCFG_128x128, 105)) return GCFG_128x128;
     // int8, 64 groups of 64 rows: 73.9 against 79.1 on 128 x 128 tiles; MXFP4
-    // 256 x 14336 x 4096: 19.2 against 20.1
-    if (mean >= 24 && fills(GCFG_64x128, 150)) return GCFG_64x128;
+    // 256 x 14336 x 4096: 19.2 against 20.1; binary16, whose stage holds half
+    // the k, keeps the deeper ring below 96 rows (64 groups of 25 rows, N =
+    // 1500: 87.9 against 110)
+    const bool f16 = kind == KIND_F16;
+    if (mean >= (f16 ? 96 : 24) && fills(GCFG_64x128, 150)) return GCFG_64x128;
     // up to two tiles per CU: the deeper ring (MXFP4 512 x 4096 x 14336 34.1
     // against 37.9); beyond that: more workgroups (8 groups of 64 rows, N =
     // 4096: 12.9 against 16.3)
-    if (fills(GCFG_64x64_S2, 201)) return GCFG_64x64_S2;
-    if (fills(GCFG_64x64_S4, 60) || used > 1) return GCFG_64x64_S4;
+    if (!f16 && fills(GCFG_64x64_S2, 201)) return GCFG_64x64_S2;
+    if (fills(GCFG_64x64_S4, 60)) return GCFG_64x64_S4;
   }
   // the lowest tile that keeps the workgroups near one per CU, up to what the
   // rows need (MXFP4 16 x 4096 x 4096: 8 rows 5.2 us, 16 rows 6.0; 32 rows
   // there: 8 rows 6.6, 16 rows 5.9; 64 rows: 32 rows 6.6, 16 rows 7.4)
   if (used == 1 ? mean <= 8 || !fills(GCFG_SKINNY_8, 126) : mean <= (kind == KIND_F16 ? 2 : 4))
     return fills(GCFG_SKINNY_8, 201) ? GCFG_SKINNY_8 : GCFG_SKINNY_8_DEEP;
-  if (used == 1 ? mean <= 16 || !fills(GCFG_SKINNY_16, 126) : mean <= 8 || kind != KIND_F16) return GCFG_SKINNY_16;
+  if (used == 1 ? mean <= 16 || !fills(GCFG_SKINNY_16, 126) : mean <= (kind == KIND_F16 ? 8 : 12))
+    return GCFG_SKINNY_16;
   return GCFG_SKINNY_32;
+}
+
+// Columns per workgroup of the narrow kernels: of 32, 28, 24 and 16 the width
+// that leaves the busiest CU the fewest columns, for t row tiles (N = 14336 in
+// one row tile: 512 workgroups of 28 columns, two per CU, instead of 448 of
+// 32: MXFP4 16 rows 8.4 against 8.7 us; N = 4096: 256 of 16 instead of 128,
+// 4.8 against 5.1).  The wider on equal terms: every workgroup reads its rows
+// of A.
+inline int grouped_columns(int64_t t, int64_t N, int cu_count) {
+  int best = 32;
+  int64_t least = INT64_MAX;
+  for (int w : {32, 28, 24, 16}) {
+    const int64_t load = (t * tiles(N, w) + cu_count - 1) / cu_count * w;
+    if (load < least) {
+      least = load;
+      best = w;
+    }
+  }
+  return best;
 }
 
 template <int KIND>
@@ -98,7 +124,12 @@ template <int KIND>
 lpgemm_status run_grouped(GroupedArgs p, int cu_count, hipStream_t stream) {
   const GroupedCfg cfg = choose_grouped(KIND, p.rows, p.groups, p.N, cu_count);
   p.k_stages = (p.row_bytes + 127) / 128;
-  p.tiles_n = tiles(p.N, grouped_tile_cols(cfg));
+  p.tile_w = grouped_tile_cols(cfg);
+  // (where the number of row tiles is known: one group, or about one row per
+  // expert of a token)
+  if (cfg <= GCFG_SKINNY_32 && (p.groups == 1 || p.rows <= 8))
+    p.tile_w = grouped_columns(p.groups == 1 ? tiles(p.rows, grouped_tile_rows(cfg)) : p.rows, p.N, cu_count);
+  p.tiles_n = tiles(p.N, p.tile_w);
   const int64_t grid = grouped_max_tiles(p.rows, p.groups, grouped_tile_rows(cfg)) * p.tiles_n;
   if (grid > INT32_MAX) return LPGEMM_ERROR_UNSUPPORTED_SHAPE;
   const void* fn = nullptr;

@@ -42,6 +42,7 @@ struct GroupedArgs {
   int scale_stride;
   int k_stages;              // 128-byte K-stages
   int tiles_n;
+  int tile_w;                // grouped_skinny: columns per workgroup, at most 32
 };
 
 // This workgroup's tile: rows [row0, row_end) of C (at most the tile's), all
@@ -622,8 +623,8 @@ __global__ __launch_bounds__(WAVES * 64) void grouped_skinny(GroupedArgs p) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const GroupTile tile = find_tile<MT>(p, blockIdx.x);
   if (tile.none) return;
-  const int n0 = tile.tn * 32;
-  const int cols = min(32, p.N - n0);
+  const int n0 = tile.tn * p.tile_w;
+  const int cols = min(p.tile_w, p.N - n0);
   const size_t brow0 = (size_t)tile.group * p.N + n0;
   const bool gather = p.row_index != nullptr;
   const size_t arow0 = gather ? 0 : tile.row0;
