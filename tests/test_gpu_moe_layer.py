@@ -1,0 +1,42 @@
+"""GPU: the example's mixture-of-experts layer against float64 on the same
+quantised weights.
+
+int8 rounds each activation to within 1/254 of its row's largest value; with
+rows of a few hundred normal values (largest about 3.5 times the root mean
+square) that is a relative error of about 3.5 / 127 / sqrt(12) = 0.8% per
+rounding, twice in the layer, and the bf16 intermediates add less; MXFP4 (a
+grid of 8 magnitudes: up to 1/6 of a value, about 7-10% in the mean square)
+rounds the same two tensors, and its activations also to int8.  The bounds
+leave a factor of two."""
+import os
+import sys
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+import moe_layer  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+@pytest.mark.parametrize("fmt,bound", [("w8a8", 0.03), ("mxfp4", 0.3)])
+@pytest.mark.parametrize("T", [1, 7, 150])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_layer(fmt, bound, T, dtype):
+    print("[case] layer", fmt, T, dtype, flush=True)
+    layer = moe_layer.random_layer(12, 512, 288, 3, fmt, dtype, seed=T)
+    g = torch.Generator(device="cuda").manual_seed(T)
+    x = torch.randn(T, 512, generator=g, device="cuda").to(dtype)
+    r = torch.randn(T, 512, generator=g, device="cuda").to(dtype)
+    out, h = layer(x, r)
+    ref, href = layer.plain(x, r)
+    assert out.dtype == dtype and torch.equal(h, href)
+    assert ((out.double() - ref).norm() / ref.norm()).item() < bound
