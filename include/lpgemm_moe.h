@@ -142,6 +142,20 @@ lpgemm_status lpgemm_mxfp4_grouped(int64_t rows, int64_t groups, int64_t N, int6
                                    const int32_t *row_index, lpgemm_type type, void *C,
                                    hipStream_t stream);
 
+/* Ablation hook, as lpgemm_force_config: the grouped and MXFP4 products have
+ * lpgemm_grouped_config_count() kernels, of which every call takes one by its
+ * sizes.  lpgemm_force_grouped_config(c) pins kernel c for every later call in
+ * the process, or restores the choice for any other value (-1), and returns
+ * the previous setting (-1 = by size).  Every kernel computes every size; the
+ * integer results do not depend on it, the order of the others' sums does.
+ * lpgemm_grouped_auto_config tells the choice for a device with `cu_count`
+ * compute units: kind 2 lpgemm_f16_grouped, 3 lpgemm_i8_dequant_grouped, 6
+ * MXFP4 (groups = 1: also lpgemm_mxfp4); -1 for other kinds, empty sizes or
+ * sizes out of range.  Host arithmetic only. */
+int lpgemm_grouped_config_count(void);
+int lpgemm_force_grouped_config(int config);
+int lpgemm_grouped_auto_config(int kind, int64_t rows, int64_t groups, int64_t N, int cu_count);
+
 #ifdef __cplusplus
 }
 #endif

@@ -29,7 +29,8 @@ __all__ = ["LpgemmError", "gemm_i8", "gemm_i8_kxn", "gemm_i4", "gemm_f16", "gemm
 
 # the expert-layer operators, imported with torch on their first use
 _MOE = ("add_rmsnorm_quantize", "silu_mul_quantize", "quantize_mxfp4", "dequantize_mxfp4", "mxfp4_scale_stride",
-        "gemm_mxfp4", "gemm_i8_dequant_grouped", "gemm_f16_grouped", "gemm_mxfp4_grouped")
+        "gemm_mxfp4", "gemm_i8_dequant_grouped", "gemm_f16_grouped", "gemm_mxfp4_grouped", "grouped_config_count",
+        "force_grouped_config", "grouped_auto_config")
 __all__ += _MOE
 
 

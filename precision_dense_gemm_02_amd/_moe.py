@@ -48,6 +48,28 @@ def _function(name: str):
     return f
 
 
+def grouped_config_count() -> int:
+    """Number of kernels the grouped and MXFP4 products choose from."""
+    return int(load_library().lpgemm_grouped_config_count())
+
+
+def force_grouped_config(config: int) -> int:
+    """Pin kernel `config` for later grouped and MXFP4 products in this process
+    (-1: by size); returns the previous setting."""
+    return int(load_library().lpgemm_force_grouped_config(int(config)))
+
+
+GROUPED_KINDS = {"f16": 2, "i8": 3, "mxfp4": 6}
+
+
+def grouped_auto_config(kind: str, rows: int, groups: int, N: int, cu_count: int) -> int:
+    """The kernel a grouped product of `kind` ("i8", "f16" or "mxfp4") takes on
+    `cu_count` compute units (-1: nothing is launched or out of range)."""
+    f = load_library().lpgemm_grouped_auto_config
+    f.argtypes = [_int, _i64, _i64, _i64, _int]
+    return int(f(GROUPED_KINDS[kind], rows, groups, N, cu_count))
+
+
 def _stream_of(index: int) -> int:
     return torch.cuda.current_stream(index).cuda_stream
 

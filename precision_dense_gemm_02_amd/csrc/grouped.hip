@@ -2,6 +2,10 @@
 // (include/lpgemm_moe.h).
 #include "grouped.hpp"
 
+namespace lpgemm {
+std::atomic<int> g_forced_grouped{-1};
+}  // namespace lpgemm
+
 using namespace lpgemm;
 
 namespace {
@@ -116,6 +120,18 @@ lpgemm_status lpgemm_mxfp4_grouped(int64_t rows, int64_t groups, int64_t N, int6
 lpgemm_status lpgemm_mxfp4(int64_t M, int64_t N, int64_t K, const uint8_t* A, const uint8_t* A_scale,
                            const uint8_t* B, const uint8_t* B_scale, lpgemm_type type, void* C, hipStream_t stream) {
   return mxfp4(M, 1, N, K, M, A, A_scale, B, B_scale, false, nullptr, nullptr, type, C, stream);
+}
+
+int lpgemm_grouped_config_count(void) { return GCFG_COUNT; }
+
+int lpgemm_force_grouped_config(int config) {
+  return g_forced_grouped.exchange(config >= 0 && config < GCFG_COUNT ? config : -1);
+}
+
+int lpgemm_grouped_auto_config(int kind, int64_t rows, int64_t groups, int64_t N, int cu_count) {
+  if ((kind != KIND_F16 && kind != KIND_I8_DEQUANT && kind != KIND_MXFP4) || cu_count < 1) return -1;
+  if (rows <= 0 || groups <= 0 || N <= 0 || rows > INT32_MAX || groups > LPGEMM_MAX_GROUPS || N > INT32_MAX) return -1;
+  return (int)choose_grouped(kind, rows, groups, N, cu_count);
 }
 
 }  // extern "C"

@@ -116,13 +116,19 @@ inline int grouped_columns(int64_t t, int64_t N, int cu_count) {
   return best;
 }
 
+// The kernel pinned by lpgemm_force_grouped_config, -1 for the choice above
+// (grouped.hip).
+extern std::atomic<int> g_forced_grouped;
+
 template <int KIND>
 lpgemm_status run_grouped(GroupedArgs p, int cu_count, hipStream_t stream);
 
 #ifdef LPGEMM_GROUPED_DEFINE
 template <int KIND>
 lpgemm_status run_grouped(GroupedArgs p, int cu_count, hipStream_t stream) {
-  const GroupedCfg cfg = choose_grouped(KIND, p.rows, p.groups, p.N, cu_count);
+  const int forced = g_forced_grouped.load(std::memory_order_relaxed);
+  GroupedCfg cfg = forced >= 0 ? (GroupedCfg)forced : choose_grouped(KIND, p.rows, p.groups, p.N, cu_count);
+  if (KIND == KIND_F16 && cfg == GCFG_64x64_S2) cfg = GCFG_64x64_S4;   // binary16 has the deeper ring only
   p.k_stages = (p.row_bytes + 127) / 128;
   p.tile_w = grouped_tile_cols(cfg);
   // (where the number of row tiles is known: one group, or about one row per
@@ -139,7 +145,9 @@ lpgemm_status run_grouped(GroupedArgs p, int cu_count, hipStream_t stream) {
     case GCFG_SKINNY_16: fn = (const void*)&grouped_skinny<KIND, 4, 2, 2>; break;
     case GCFG_SKINNY_32: fn = (const void*)&grouped_skinny<KIND, 4, 2, 4>; break;
     case GCFG_64x64_S4: fn = (const void*)&grouped_tile<KIND, 64, 64, 2, 2, 4, false, false>; break;
-    case GCFG_64x64_S2: fn = (const void*)&grouped_tile<KIND, 64, 64, 2, 2, 2, false, false>; break;
+    case GCFG_64x64_S2:
+      if constexpr (KIND != KIND_F16) fn = (const void*)&grouped_tile<KIND, 64, 64, 2, 2, 2, false, false>;
+      break;
     case GCFG_64x128: fn = (const void*)&grouped_tile<KIND, 64, 128, 1, 4, 2, false, false>; break;
     case GCFG_128x128: fn = (const void*)&grouped_tile<KIND, 128, 128, 2, 2, 2, false, true>; break;
     default: fn = (const void*)&grouped_tile<KIND, 256, 256, 2, 2, 2, true, true>; break;

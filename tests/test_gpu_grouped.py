@@ -217,6 +217,62 @@ def test_weights_and_results_past_4_gib():
         assert torch.equal(c[rows_], (a[rows_].double() @ w.double().t()).float())
 
 
+# every kernel at sizes that end inside its tile, its stage and its ring:
+# rows of groups around every tile height and around the 32- and 64-row steps
+# in which a partial tile of 128 and 256 rows runs; N below, at and past the
+# tile widths and odd; K of one step to three more stages than the deepest
+# ring holds, whole and partial
+CONFIGS = range(9)
+FORCED = [((1, 0, 7), 33, 1), ((8, 9, 16, 17), 70, 7), ((31, 33, 1, 64), 129, 31), ((65, 127, 128), 64, 17),
+          ((129, 190, 3), 257, 40), ((255, 256, 60), 300, 9), ((257, 70, 320, 450), 260, 26), ((520, 5), 513, 12)]
+
+
+@pytest.fixture(params=CONFIGS)
+def forced(request):
+    assert lp.grouped_config_count() == len(CONFIGS)
+    previous = lp.force_grouped_config(request.param)
+    yield request.param
+    lp.force_grouped_config(previous)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_every_kernel(kind, forced):
+    for counts, N, ksteps in FORCED:
+        K = ksteps * K_STEP[kind]
+        rows = sum(counts)
+        t = ("f32", "f16", "bf16")[(rows + forced) % 3]
+        print("[case] kernel", forced, kind, counts, N, K, t, flush=True)
+        p = Problem(kind, 50, len(counts), N, K, seed=rows)
+        offsets = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+        index = p.rng.integers(0, 50, rows).astype(np.int32)
+        index[rows // 2] = 50                       # one row of zeros
+        p.check(p.run(offsets, index, t), offsets, index, t)
+
+
+@pytest.mark.parametrize("M", [1, 17, 64, 100, 190, 256, 330])
+def test_every_kernel_mxfp4(M, forced):
+    rng = np.random.default_rng(M)
+    for N, K in ((31, 32), (260, 288), (513, 2080)):
+        print("[case] mxfp4 kernel", forced, M, N, K, flush=True)
+        a, as_ = ref.mx_random(rng, M, K)
+        b, bs = ref.mx_random(rng, N, K)
+        c = ref.to64(lp.gemm_mxfp4(_dev(a), _dev(as_), _dev(b), _dev(bs)))
+        av, bv = ref.mx_values(a, as_, K), ref.mx_values(b, bs, K)
+        check_sums(c, av @ bv.T, np.abs(av) @ np.abs(bv).T, K / 64, "f32")
+
+
+def test_every_kernel_mxfp4_scales(forced):
+    """Scales of every size, NaN scales and padding bytes in every kernel."""
+    test_mxfp4_scales_of_every_size(300)
+    test_mxfp4_nan_scale(200)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_every_kernel_k_zero_and_untouched_rows(kind, forced):
+    test_empty_sizes(kind)
+    test_rows_outside_groups_and_bad_routing(kind, 300, 4)
+
+
 # ------------------------------------------------------------ MXFP4 product
 
 MX_SHAPES = [(1, 1, 32), (1, 33, 64), (16, 70, 4096), (9, 300, 544), (33, 100, 96), (64, 129, 2880), (100, 257, 1024),

@@ -141,3 +141,26 @@ def test_binding_refuses_host_tensors_and_types():
         lp.gemm_f16_grouped(x.float(), x[None], None)
     with pytest.raises(AttributeError):
         lp.no_such_operator
+
+
+def test_grouped_configs():
+    """The choice by size, pinned where a measured rule changes it (256 CUs)."""
+    n = lp.grouped_config_count()
+    assert lp.force_grouped_config(n) == -1 and lp.force_grouped_config(2) == -1
+    assert lp.force_grouped_config(-1) == 2 and lp.force_grouped_config(-1) == -1
+    rules = [
+        # one group: few rows, narrow tiles by how many workgroups they make
+        ("mxfp4", 1, 1, 4096, 0), ("mxfp4", 16, 1, 4096, 0), ("mxfp4", 8, 1, 20000, 1), ("mxfp4", 16, 1, 14336, 2),
+        ("mxfp4", 32, 1, 4096, 2), ("mxfp4", 64, 1, 4096, 3), ("mxfp4", 64, 1, 14336, 4), ("mxfp4", 512, 1, 4096, 4),
+        ("mxfp4", 768, 1, 4096, 6), ("mxfp4", 1024, 1, 2048, 4), ("mxfp4", 192, 1, 14336, 5), ("mxfp4", 256, 1, 14336, 6),
+        ("mxfp4", 3000, 1, 1536, 7), ("mxfp4", 2048, 1, 4096, 7), ("mxfp4", 4096, 1, 4096, 8), ("mxfp4", 8192, 1, 8192, 8),
+        # experts: by the mean of their rows
+        ("i8", 8, 64, 2048, 0), ("i8", 64, 64, 2048, 1), ("i8", 512, 64, 2048, 2), ("i8", 1024, 64, 2048, 5),
+        ("i8", 2048, 64, 2048, 6), ("i8", 4096, 64, 2048, 7), ("i8", 8192, 8, 14336, 8), ("i8", 60, 4, 2048, 3),
+        ("mxfp4", 512, 64, 2048, 5), ("mxfp4", 256, 64, 2048, 1), ("mxfp4", 300, 64, 2048, 2),
+        ("f16", 1000, 64, 2048, 3), ("f16", 500, 64, 2048, 2), ("f16", 2048, 64, 2048, 4), ("f16", 6400, 64, 1500, 7),
+    ]
+    got = [(*r[:4], lp.grouped_auto_config(*r[:4], 256)) for r in rules]
+    assert got == rules
+    for bad in (("i8", 0, 1, 1, 256), ("i8", 1, 0, 1, 256), ("i8", 1, 1, 0, 256), ("i8", 1, 1, 1, 0), ("i8", 2 ** 31, 1, 1, 256)):
+        assert lp.grouped_auto_config(*bad) == -1
