@@ -99,7 +99,9 @@ lpgemm_status lpgemm_dequantize_mxfp4(int64_t rows, int64_t K, const uint8_t *co
 /* C = A . B for two MXFP4 operands (A: M x K, B: N x K, each with its
  * scales), summed in binary32 by the chip's scaled matrix instructions;
  * C: M x N of `type`.  The order of the sum depends on the sizes only.
- * Pointers 16-byte aligned.  M = 0 or N = 0 is a no-op; K = 0 sets C to 0. */
+ * M and N at most 2^31 - 257, and below 2^24 tiles of C (UNSUPPORTED_SHAPE
+ * otherwise).  Pointers 16-byte aligned.  M = 0 or N = 0 is a no-op; K = 0
+ * sets C to 0. */
 lpgemm_status lpgemm_mxfp4(int64_t M, int64_t N, int64_t K, const uint8_t *A, const uint8_t *A_scale,
                            const uint8_t *B, const uint8_t *B_scale, lpgemm_type type, void *C,
                            hipStream_t stream);
@@ -118,7 +120,9 @@ lpgemm_status lpgemm_mxfp4(int64_t M, int64_t N, int64_t K, const uint8_t *A, co
  * With a row_index the tokens A must stay below 2 GiB (UNSUPPORTED_SHAPE).
  * groups = 0, rows = 0 or N = 0 is a no-op; K = 0 sets the grouped rows to 0;
  * a_rows = 0 with rows > 0 needs a row_index and gives rows of zeros.
- * groups is at most LPGEMM_MAX_GROUPS.  A, B and C 16-byte aligned, offsets,
+ * groups is at most LPGEMM_MAX_GROUPS, rows and N at most 2^31 - 257, and the
+ * tiles of C must fit one launch (below 2^24 workgroups; UNSUPPORTED_SHAPE
+ * otherwise).  A, B and C 16-byte aligned, offsets,
  * row_index and fp32 scales 4-byte.
  *
  * lpgemm_i8_dequant_grouped: A a_rows x K int8, row_scale a_rows floats (one

@@ -23,6 +23,8 @@ lpgemm_status check(int64_t rows, int64_t groups, int64_t N, int64_t K, int64_t 
   if (rows > INT32_MAX || N > INT32_MAX || a_rows > INT32_MAX || !c_type(type)) return LPGEMM_ERROR_INVALID_VALUE;
   if (rows > 0 && !row_index && a_rows != rows) return LPGEMM_ERROR_INVALID_VALUE;
   if (K % k_by != 0 || K > k_max || groups > LPGEMM_MAX_GROUPS) return LPGEMM_ERROR_UNSUPPORTED_SHAPE;
+  // (a tile's last row and column must not leave 32 bits)
+  if (rows > INT32_MAX - 256 || N > INT32_MAX - 256) return LPGEMM_ERROR_UNSUPPORTED_SHAPE;
   if (row_index && a_rows * row_bytes >= ((int64_t)1 << 31)) return LPGEMM_ERROR_UNSUPPORTED_SHAPE;
   if (rows == 0 || groups == 0 || N == 0) {
     nothing = true;

@@ -137,7 +137,7 @@ lpgemm_status run_grouped(GroupedArgs p, int cu_count, hipStream_t stream) {
     p.tile_w = grouped_columns(p.groups == 1 ? tiles(p.rows, grouped_tile_rows(cfg)) : p.rows, p.N, cu_count);
   p.tiles_n = tiles(p.N, p.tile_w);
   const int64_t grid = grouped_max_tiles(p.rows, p.groups, grouped_tile_rows(cfg)) * p.tiles_n;
-  if (grid > INT32_MAX) return LPGEMM_ERROR_UNSUPPORTED_SHAPE;
+  if (grid * 256 > UINT32_MAX) return LPGEMM_ERROR_UNSUPPORTED_SHAPE;   // threads of one launch
   const void* fn = nullptr;
   switch (cfg) {
     case GCFG_SKINNY_8_DEEP: fn = (const void*)&grouped_skinny<KIND, 4, 3, 1>; break;

@@ -18,11 +18,11 @@ lpgemm_status enqueue(const void* fn, int64_t grid, int threads, void* args, hip
              : LPGEMM_ERROR_LAUNCH;
 }
 
-// The kernel for rows of K values: in registers up to 16384 values, a
+// The kernel for M rows of K values: in registers up to 16384 values, a
 // wavefront per row once the rows fill the SIMDs (up to 8192 values), else a
 // workgroup per row.
 template <typename T, bool NORM>
-lpgemm_status run_rows(RowArgs& p, int cu_count, hipStream_t stream) {
+lpgemm_status launch_rows(RowArgs& p, int cu_count, hipStream_t stream) {
   const int K = p.K;
   if (K == 0 || K > 16384) return enqueue((const void*)&rows_int8_long<T, NORM>, p.M, 1024, &p, stream);
   const bool wide = p.M < 4 * (int64_t)cu_count || K > 8192;
@@ -40,6 +40,25 @@ lpgemm_status run_rows(RowArgs& p, int cu_count, hipStream_t stream) {
          : nc <= 8 ? (const void*)&rows_int8_regs<T, NORM, 1, 8>
                    : (const void*)&rows_int8_regs<T, NORM, 1, 16>;
   return enqueue(fn, wide ? p.M : ((int64_t)p.M + 3) / 4, 256, &p, stream);
+}
+
+// A grid holds less than 2^32 threads: more rows than this go out in several
+// launches.
+constexpr int64_t kRowsPerLaunch = (int64_t)1 << 21;
+
+template <typename T, bool NORM>
+lpgemm_status run_rows(RowArgs p, int64_t M, int cu_count, hipStream_t stream) {
+  lpgemm_status st = LPGEMM_SUCCESS;
+  for (int64_t r = 0; r < M && st == LPGEMM_SUCCESS; r += kRowsPerLaunch) {
+    p.M = (int)(M - r < kRowsPerLaunch ? M - r : kRowsPerLaunch);
+    st = launch_rows<T, NORM>(p, cu_count, stream);
+    p.X += kRowsPerLaunch * p.x_stride;
+    if (p.R) p.R += kRowsPerLaunch * p.r_stride;
+    if (p.H) p.H += kRowsPerLaunch * p.h_stride;
+    p.Q += kRowsPerLaunch * p.K;
+    p.scale += kRowsPerLaunch;
+  }
+  return st;
 }
 
 bool bad_stride(int64_t stride, int64_t least) { return stride < least || stride % 8 != 0; }
@@ -73,11 +92,10 @@ lpgemm_status lpgemm_add_rmsnorm_quantize(int64_t M, int64_t K, lpgemm_type type
   p.x_stride = 2 * x_stride;
   p.r_stride = 2 * r_stride;
   p.h_stride = 2 * h_stride;
-  p.M = (int)M;
   p.K = (int)K;
   p.eps = eps;
-  return type == LPGEMM_F16 ? run_rows<TypeF16, true>(p, dev.cu_count, stream)
-                            : run_rows<TypeBF16, true>(p, dev.cu_count, stream);
+  return type == LPGEMM_F16 ? run_rows<TypeF16, true>(p, M, dev.cu_count, stream)
+                            : run_rows<TypeBF16, true>(p, M, dev.cu_count, stream);
 }
 
 lpgemm_status lpgemm_silu_mul_quantize(int64_t M, int64_t K, lpgemm_type type, const void* X, int64_t x_stride,
@@ -97,10 +115,9 @@ lpgemm_status lpgemm_silu_mul_quantize(int64_t M, int64_t K, lpgemm_type type, c
   p.Q = Q;
   p.scale = row_scale;
   p.x_stride = 2 * x_stride;
-  p.M = (int)M;
   p.K = (int)K;
-  return type == LPGEMM_F16 ? run_rows<TypeF16, false>(p, dev.cu_count, stream)
-                            : run_rows<TypeBF16, false>(p, dev.cu_count, stream);
+  return type == LPGEMM_F16 ? run_rows<TypeF16, false>(p, M, dev.cu_count, stream)
+                            : run_rows<TypeBF16, false>(p, M, dev.cu_count, stream);
 }
 
 // The MXFP4 kernels index a launch's chunks of 8 values in 32 bits; more

@@ -129,6 +129,22 @@ def test_norm_rows_past_4_gib():
     _check_norm(x, r, w, 1e-6, q, s, h)
 
 
+def test_more_rows_than_one_launch():
+    """Past 2^21 rows, in two launches: the rows around the seam and the last."""
+    M, K = (1 << 21) + 5, 16
+    _case("many rows", M, K)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(M, K, generator=g, device="cuda").half()
+    r = torch.randn(M, K, generator=g, device="cuda").half()
+    w = _rows(1, K, torch.float16, 3, False)[0]
+    q, s, h = lp.add_rmsnorm_quantize(x, w.cuda(), 1e-6, residual=r)
+    for part in (slice(0, 9), slice((1 << 21) - 4, M)):
+        _check_norm(x[part].cpu(), r[part].cpu(), w, 1e-6, q[part], s[part], h[part])
+    q, s = lp.silu_mul_quantize(x)
+    for part in (slice(0, 9), slice((1 << 21) - 4, M)):
+        _check_silu(x[part].cpu(), q[part], s[part])
+
+
 def test_norm_no_rows_no_columns():
     w = torch.ones(64, dtype=torch.float16, device="cuda")
     q, s, h = lp.add_rmsnorm_quantize(torch.empty(0, 64, dtype=torch.float16, device="cuda"), w, 1e-6)

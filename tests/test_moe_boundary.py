@@ -109,6 +109,13 @@ def test_grouped_rules(name):
         assert call(name, K=0, row_scale=None) == INVALID
 
 
+@pytest.mark.parametrize("name", GROUPED + ("lpgemm_mxfp4",))
+def test_largest_sizes(name):
+    row = "M" if name == "lpgemm_mxfp4" else "rows"
+    for size in (row, "N"):
+        assert call(name, **{size: 2 ** 31 - 256}) == SHAPE, size
+
+
 @pytest.mark.parametrize("name", sorted(DEFAULTS))
 def test_empty_problems_read_nothing(name):
     nothing = {k: None for k, v in DEFAULTS[name].items() if v == P and k != "row_index"}
