@@ -158,7 +158,7 @@ lpgemm_status lpgemm_mxfp4_grouped(int64_t rows, int64_t groups, int64_t N, int6
  * sizes out of range.  Host arithmetic only. */
 int lpgemm_grouped_config_count(void);
 int lpgemm_force_grouped_config(int config);
-int lpgemm_grouped_auto_config(int kind, int64_t rows, int64_t groups, int64_t N, int cu_count);
+int lpgemm_grouped_auto_config(int kind, int64_t rows, int64_t groups, int64_t N, int64_t K, int cu_count);
 
 #ifdef __cplusplus
 }

@@ -62,12 +62,12 @@ def force_grouped_config(config: int) -> int:
 GROUPED_KINDS = {"f16": 2, "i8": 3, "mxfp4": 6}
 
 
-def grouped_auto_config(kind: str, rows: int, groups: int, N: int, cu_count: int) -> int:
+def grouped_auto_config(kind: str, rows: int, groups: int, N: int, K: int, cu_count: int) -> int:
     """The kernel a grouped product of `kind` ("i8", "f16" or "mxfp4") takes on
     `cu_count` compute units (-1: nothing is launched or out of range)."""
     f = load_library().lpgemm_grouped_auto_config
-    f.argtypes = [_int, _i64, _i64, _i64, _int]
-    return int(f(GROUPED_KINDS[kind], rows, groups, N, cu_count))
+    f.argtypes = [_int, _i64, _i64, _i64, _i64, _int]
+    return int(f(GROUPED_KINDS[kind], rows, groups, N, K, cu_count))
 
 
 def _stream_of(index: int) -> int:

@@ -130,10 +130,12 @@ int lpgemm_force_grouped_config(int config) {
   return g_forced_grouped.exchange(config >= 0 && config < GCFG_COUNT ? config : -1);
 }
 
-int lpgemm_grouped_auto_config(int kind, int64_t rows, int64_t groups, int64_t N, int cu_count) {
+int lpgemm_grouped_auto_config(int kind, int64_t rows, int64_t groups, int64_t N, int64_t K, int cu_count) {
   if ((kind != KIND_F16 && kind != KIND_I8_DEQUANT && kind != KIND_MXFP4) || cu_count < 1) return -1;
   if (rows <= 0 || groups <= 0 || N <= 0 || rows > INT32_MAX || groups > LPGEMM_MAX_GROUPS || N > INT32_MAX) return -1;
-  return (int)choose_grouped(kind, rows, groups, N, cu_count);
+  if (K < 0 || K > INT32_MAX / 2) return -1;
+  const int64_t row_bytes = kind == KIND_F16 ? 2 * K : (kind == KIND_MXFP4 ? K / 2 : K);
+  return (int)choose_grouped(kind, rows, groups, N, row_bytes, cu_count);
 }
 
 }  // extern "C"

@@ -20,15 +20,17 @@ enum GroupedCfg {
   GCFG_64x128 = 6,
   GCFG_128x128 = 7,
   GCFG_256x256 = 8,
-  GCFG_COUNT = 9
+  GCFG_64x64_NT = 9,       // as 5 and 7, with B streamed non-temporally
+  GCFG_128x128_NT = 10,    // (MXFP4; the other kinds run 5 and 7)
+  GCFG_COUNT = 11
 };
 
 inline int grouped_tile_rows(int cfg) {
-  constexpr int rows[GCFG_COUNT] = {8, 8, 16, 32, 64, 64, 64, 128, 256};
+  constexpr int rows[GCFG_COUNT] = {8, 8, 16, 32, 64, 64, 64, 128, 256, 64, 128};
   return rows[cfg];
 }
 inline int grouped_tile_cols(int cfg) {
-  constexpr int cols[GCFG_COUNT] = {32, 32, 32, 32, 64, 64, 128, 128, 256};
+  constexpr int cols[GCFG_COUNT] = {32, 32, 32, 32, 64, 64, 128, 128, 256, 64, 128};
   return cols[cfg];
 }
 
@@ -47,7 +49,7 @@ inline int64_t grouped_max_tiles(int64_t rows, int64_t groups, int tile) {
 // tokens, 2 or 8 experts each), N = 768 to 14336, K = 2048 to 14336 (graph
 // replay, one MI355X; the figures at each rule are us with the kernel it
 // takes against the next best).
-inline GroupedCfg choose_grouped(int kind, int64_t rows, int64_t groups, int64_t N, int cu_count) {
+inline GroupedCfg choose_grouped(int kind, int64_t rows, int64_t groups, int64_t N, int64_t row_bytes, int cu_count) {
   const int64_t used = groups < rows ? groups : rows;
   const int64_t mean = (rows + used - 1) / used;
   // tiles of a configuration, and whether they reach `percent` of the CUs
@@ -56,6 +58,16 @@ inline GroupedCfg choose_grouped(int kind, int64_t rows, int64_t groups, int64_t
     const int64_t t = used == 1 ? tiles(rows, grouped_tile_rows(c)) : ragged > most ? ragged : most;
     return 100 * t * tiles(N, grouped_tile_cols(c)) >= percent * cu_count;
   };
+  // MXFP4 experts whose weights are more than the 256 MiB Infinity Cache keeps
+  // from one call to the next, and mostly read by one row tile: B streams
+  // non-temporally (64 experts of 2048 x 4096: 24 rows each 56.2 against 61.8
+  // us, 12 rows 50.8 against 54.4; 128 of 1024 x 2048, 24 rows 35.4 against
+  // 37.2; at 67 MB of weights 1.3-1.4 times slower, and with rows that do not
+  // start on a cache line 1.25 times: each line is fetched twice)
+  if (kind == KIND_MXFP4 && used > 1 && row_bytes % 128 == 0 && groups * N * row_bytes >= (int64_t)100 << 20) {
+    if (mean > 16 && mean < 96) return GCFG_128x128_NT;
+    if (mean > 4 && mean <= 16) return GCFG_64x64_NT;
+  }
   // few rows per group: the weights' stream is the work, and narrow tiles
   // whose waves split K keep most of it in flight (int8, 8 tokens over 64
   // experts of 2048 x 2048: 22.9 against 25.4 us on 64 x 64 tiles; MXFP4,
@@ -127,7 +139,9 @@ lpgemm_status run_grouped(GroupedArgs p, int cu_count, hipStream_t stream);
 template <int KIND>
 lpgemm_status run_grouped(GroupedArgs p, int cu_count, hipStream_t stream) {
   const int forced = g_forced_grouped.load(std::memory_order_relaxed);
-  GroupedCfg cfg = forced >= 0 ? (GroupedCfg)forced : choose_grouped(KIND, p.rows, p.groups, p.N, cu_count);
+  GroupedCfg cfg = forced >= 0 ? (GroupedCfg)forced : choose_grouped(KIND, p.rows, p.groups, p.N, p.row_bytes, cu_count);
+  if (KIND != KIND_MXFP4 && cfg == GCFG_64x64_NT) cfg = GCFG_64x64_S2;
+  if (KIND != KIND_MXFP4 && cfg == GCFG_128x128_NT) cfg = GCFG_128x128;
   if (KIND == KIND_F16 && cfg == GCFG_64x64_S2) cfg = GCFG_64x64_S4;   // binary16 has the deeper ring only
   p.k_stages = (p.row_bytes + 127) / 128;
   p.tile_w = grouped_tile_cols(cfg);
@@ -147,6 +161,12 @@ lpgemm_status run_grouped(GroupedArgs p, int cu_count, hipStream_t stream) {
     case GCFG_64x64_S4: fn = (const void*)&grouped_tile<KIND, 64, 64, 2, 2, 4, false, false>; break;
     case GCFG_64x64_S2:
       if constexpr (KIND != KIND_F16) fn = (const void*)&grouped_tile<KIND, 64, 64, 2, 2, 2, false, false>;
+      break;
+    case GCFG_64x64_NT:
+      if constexpr (KIND == KIND_MXFP4) fn = (const void*)&grouped_tile<KIND, 64, 64, 2, 2, 2, false, false, true>;
+      break;
+    case GCFG_128x128_NT:
+      if constexpr (KIND == KIND_MXFP4) fn = (const void*)&grouped_tile<KIND, 128, 128, 2, 2, 2, false, true, true>;
       break;
     case GCFG_64x128: fn = (const void*)&grouped_tile<KIND, 64, 128, 1, 4, 2, false, false>; break;
     case GCFG_128x128: fn = (const void*)&grouped_tile<KIND, 128, 128, 2, 2, 2, false, true>; break;

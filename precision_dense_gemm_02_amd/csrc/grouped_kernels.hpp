@@ -230,7 +230,9 @@ __device__ __forceinline__ void store1(const GroupedArgs& p, size_t idx, float v
 // rows are left out.  There the waves' rows alternate by block, so that the
 // blocks fall on all of them; in a whole tile each wave has one run of rows
 // (alternating there too took 8192^3 from 272 to 279 us).  Needs two stages.
-template <int KIND, int BM, int BN, int WM, int WN, int STAGES, bool PIN, bool TAIL>
+//
+// BNT: B streams non-temporally, where it is read once.
+template <int KIND, int BM, int BN, int WM, int WN, int STAGES, bool PIN, bool TAIL, bool BNT = false>
 __global__ __launch_bounds__(256) void grouped_tile(GroupedArgs p) {
   using Acc = typename GroupedAcc<KIND>::type;
   using Layout = RowLayout<128>;
@@ -320,7 +322,7 @@ __global__ __launch_bounds__(256) void grouped_tile(GroupedArgs p) {
     const uint32_t off = kbyte + slot_col < (uint32_t)p.row_bytes ? slot_off[t] + kbyte : kOutOfRange;
     const uint32_t to = smem_lds + (s % STAGES) * kStage + (4 * t + wave) * 1024;
     if (t < kSlotsA) lds_dma_16(rsrc_a, to, off);
-    else lds_dma_16(rsrc_b, to, off);
+    else lds_dma_16<BNT ? 1 : 0>(rsrc_b, to, off);
   };
   auto issue_scales = [&](int s) {   // s a multiple of 4: blocks 8 s .. 8 s + 31 of every row
     if constexpr (MX) {

@@ -222,7 +222,7 @@ def test_weights_and_results_past_4_gib():
 # in which a partial tile of 128 and 256 rows runs; N below, at and past the
 # tile widths and odd; K of one step to three more stages than the deepest
 # ring holds, whole and partial
-CONFIGS = range(9)
+CONFIGS = range(11)
 FORCED = [((1, 0, 7), 33, 1), ((8, 9, 16, 17), 70, 7), ((31, 33, 1, 64), 129, 31), ((65, 127, 128), 64, 17),
           ((129, 190, 3), 257, 40), ((255, 256, 60), 300, 9), ((257, 70, 320, 450), 260, 26), ((520, 5), 513, 12)]
 

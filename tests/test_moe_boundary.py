@@ -167,7 +167,12 @@ def test_grouped_configs():
         ("mxfp4", 512, 64, 2048, 5), ("mxfp4", 256, 64, 2048, 1), ("mxfp4", 300, 64, 2048, 2),
         ("f16", 1000, 64, 2048, 3), ("f16", 500, 64, 2048, 2), ("f16", 2048, 64, 2048, 4), ("f16", 6400, 64, 1500, 7),
     ]
-    got = [(*r[:4], lp.grouped_auto_config(*r[:4], 256)) for r in rules]
+    got = [(*r[:4], lp.grouped_auto_config(*r[:4], 1024, 256)) for r in rules]
     assert got == rules
-    for bad in (("i8", 0, 1, 1, 256), ("i8", 1, 0, 1, 256), ("i8", 1, 1, 0, 256), ("i8", 1, 1, 1, 0), ("i8", 2 ** 31, 1, 1, 256)):
+    # MXFP4 experts of more than 100 MiB, rows on cache lines: streamed
+    for rows, K, config in ((256, 4096, 1), (512, 4096, 9), (1024, 4096, 9), (2048, 4096, 10), (5000, 4096, 10),
+                            (6200, 4096, 7), (2048, 4128, 6), (2048, 1024, 6)):
+        assert lp.grouped_auto_config("mxfp4", rows, 64, 2048, K, 256) == config, (rows, K)
+    for bad in (("i8", 0, 1, 1, 16, 256), ("i8", 1, 0, 1, 16, 256), ("i8", 1, 1, 0, 16, 256), ("i8", 1, 1, 1, -1, 256),
+                ("i8", 1, 1, 1, 16, 0), ("i8", 2 ** 31, 1, 1, 16, 256)):
         assert lp.grouped_auto_config(*bad) == -1
