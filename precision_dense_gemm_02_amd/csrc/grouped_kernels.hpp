@@ -247,9 +247,12 @@ __global__ __launch_bounds__(256) void grouped_tile(GroupedArgs p) {
   constexpr int kSlotsA = BM / 32;
   constexpr int kSc = MX ? (kRows / 32 + 3) / 4 : 0;   // scale loads per wave, every fourth stage (32 rows each)
   constexpr int kScBuf = kSc * 4096;
-  // (two buffers: the one filled during stage 4 e + 5 - STAGES was last read
-  // at the end of stage 4 e - 2)
-  static_assert(!MX || (STAGES >= 2 && STAGES <= 6), "scale buffers");
+  // Two buffers.  The scales of stages 4 e + 4 .. 4 e + 7 are fetched at the
+  // start of stage 4 e + 1, into the buffer last read during stage 4 e - 2.
+  // They are read from stage 4 e + 3 on, and have landed by the end of stage
+  // 4 e + 2: at most the loads of the STAGES - 2 stages issued behind them
+  // may then be in flight.
+  static_assert(!MX || (STAGES >= 2 && STAGES <= 4), "scale buffers");
   static_assert(!TAIL || STAGES == 2, "fewer loads in flight than the waits of a longer ring count");
   constexpr int kMainLds = STAGES * kStage + 2 * kScBuf;
   constexpr int kEpiPitch = WTN * 4 + 32;
@@ -258,9 +261,9 @@ __global__ __launch_bounds__(256) void grouped_tile(GroupedArgs p) {
   constexpr int kLds = kMainLds > 4 * kEpiWave ? kMainLds : 4 * kEpiWave;
   static_assert(kLds <= 160 * 1024, "LDS");
   // loads that may be in flight once stage s + 1 has landed: those of stages
-  // s + 2 .. s + STAGES - 1, and the scales' where one of them is a fourth
+  // s + 2 .. s + STAGES - 1
   constexpr int kInFlight = (STAGES - 2) * kSlots;
-  static_assert(kInFlight + 2 * kSc <= 63, "vmcnt range");
+  static_assert(kInFlight + kSlots + kSc <= 63, "vmcnt range");
 
   __shared__ __attribute__((aligned(1024))) uint8_t smem[kLds];
 
@@ -324,26 +327,16 @@ __global__ __launch_bounds__(256) void grouped_tile(GroupedArgs p) {
     if (t < kSlotsA) lds_dma_16(rsrc_a, to, off);
     else lds_dma_16<BNT ? 1 : 0>(rsrc_b, to, off);
   };
-  auto issue_scales = [&](int s) {   // s a multiple of 4: blocks 8 s .. 8 s + 31 of every row
+  auto issue_scales = [&](int e) {   // of stages 4 e .. 4 e + 3: blocks 32 e .. 32 e + 31 of every row
     if constexpr (MX) {
-      const bool inside = 8 * s + sc_half < p.scale_stride;
+      const bool inside = 32 * e + sc_half < p.scale_stride;
 #pragma unroll
       for (int t = 0; t < kSc; ++t) {
-        const uint32_t off = inside ? sc_off[t] + 8 * s : kOutOfRange;
-        const uint32_t to = smem_lds + STAGES * kStage + ((s / 4) & 1) * kScBuf + (4 * t + wave) * 1024;
+        const uint32_t off = inside ? sc_off[t] + 32 * e : kOutOfRange;
+        const uint32_t to = smem_lds + STAGES * kStage + (e & 1) * kScBuf + (4 * t + wave) * 1024;
         if (32 * (4 * t + wave) < BM) lds_dma_16(rsrc_as, to, off);
         else lds_dma_16(rsrc_bs, to, off);
       }
-    }
-  };
-  // own loads of stage s + 1 have landed
-  auto wait_stage = [&](int s) {
-    if constexpr (MX && STAGES > 2) {
-      // is one of stages s + 2 .. s + STAGES - 1 a fourth (with scales)?
-      if (((s + 1) & 3) + STAGES - 2 >= 4) wait_vmcnt<kInFlight + kSc>();
-      else wait_vmcnt<kInFlight>();
-    } else {
-      wait_vmcnt<kInFlight>();
     }
   };
 
@@ -415,14 +408,13 @@ __global__ __launch_bounds__(256) void grouped_tile(GroupedArgs p) {
       }
     };
     if (nks > 0) {
+      issue_scales(0);
 #pragma unroll
-      for (int s = 0; s < STAGES - 1; ++s) {
-        if (s % 4 == 0) issue_scales(s);
+      for (int s = 0; s < STAGES - 1; ++s)
 #pragma unroll
         for (int t = 0; t < kSlots; ++t)
           if (used(t)) issue_load(t, s);
-      }
-      wait_stage(-1);
+      wait_vmcnt<kInFlight>();
       block_barrier();
       read_frags(0, 0, 0);
       read_scales(0);
@@ -448,7 +440,7 @@ __global__ __launch_bounds__(256) void grouped_tile(GroupedArgs p) {
         constexpr int src = kk & 1, dst = src ^ 1;
         int nl = 0, pre = 0;
         if constexpr (kk == 0) {
-          if (MX && (sl & 3) == 0) issue_scales(sl);
+          if (MX && (s & 3) == 1) issue_scales(s / 4 + 1);
         }
         if constexpr (kk < kLoadSteps) {
 #pragma unroll
@@ -470,17 +462,17 @@ __global__ __launch_bounds__(256) void grouped_tile(GroupedArgs p) {
         }
         if constexpr (kk < 3) {
           read_frags(s, kk + 1, dst);
+          if constexpr (kk == 1) read_scales(s + 1);
           compute(kk_c, src, pre, kMfma);
-          interleave(kMfma - pre, kReads, nl);
+          interleave(kMfma - pre, kk == 1 && MX ? 2 * kReads : kReads, nl);
         } else {
           compute(kk_c, src, 0, kSplit);
           interleave(kSplit, 0, 0);
           __builtin_amdgcn_sched_barrier(0);
-          wait_stage(s);             // own loads of stage s + 1 landed
+          wait_vmcnt<kInFlight>();   // own loads of stage s + 1 landed
           wait_lgkmcnt0();           // own reads of stage s done
           block_barrier();           // ... everyone's
           read_frags(s + 1, 0, dst);
-          read_scales(s + 1);
           compute(kk_c, src, kSplit, kMfma);
           interleave(kMfma - kSplit, kReads, 0);
         }
