@@ -40,7 +40,8 @@ typedef enum lpgemm_type {
  *   h   = X + R, the sum rounded to `type` (R NULL: h = X);  H = h if H is
  *         not NULL (the residual stream for the next addition);
  *   z_k = h_k * weight_k in binary32, a = max_k |z_k|;
- *   Q_k = the nearest-even integer to z_k * (127 / a), both in binary32;
+ *   Q_k = the nearest-even integer to z_k * (127 * (1 / a)), each operation
+ *         rounded to binary32;
  *   row_scale = (a / 127) / sqrt(mean_k h_k^2 + eps), in binary32,
  * so that Q_k * row_scale is the normalised, weighted row.  The norm's own
  * factor cancels out of the codes, which therefore depend on no sum.

@@ -217,13 +217,16 @@ __device__ __forceinline__ void store1(const GroupedArgs& p, size_t idx, float v
 //
 // MXFP4 scales travel with the operands: every fourth stage two 16-byte loads
 // per operand row fetch the scales of four stages (32 blocks, 32 bytes) into
-// one of two buffers of their own.  (A row's scales lie in one cache line per
-// 4096 values of k, which every fetch moves again: 16 bytes per fetch took
-// 8192^3 from 273 us without scales to 307.)
+// one of two buffers of their own (a row's scales lie in one cache line per
+// 4096 values of k, which every fetch moves again: with 16 bytes per fetch
+// 8192^3 took 307 us, without any scale loads 273), two stages ahead; they are
+// read a stage ahead, in a K-step that waits for nothing else (read behind the
+// stage barrier: 267 us against 260).
 //
-// PIN: the next stage's loads all go out in the first two K-steps, one MFMA
-// pinned in front of each (the schedule would otherwise issue them back to
-// back); without it they are spread over the first three K-steps.
+// The loads of a stage all go out in its first two K-steps (MXFP4 2048 x 4096
+// x 4096 on 128 x 128 tiles 22.4 us, over three 23.3; 8192^3 on 256 x 256 in
+// one 264, in two 250).  PIN: one MFMA is pinned in front of each (the schedule
+// would otherwise issue them back to back: 8192^3 272 us against 265).
 //
 // TAIL: a group's last tile runs the main loop for the 32-row blocks that its
 // rows reach, in steps of WM blocks; its loads and products for the other
@@ -357,7 +360,7 @@ __global__ __launch_bounds__(256) void grouped_tile(GroupedArgs p) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
 
-  constexpr int kLoadSteps = PIN ? 2 : 3;
+  constexpr int kLoadSteps = 2;
   constexpr int kLoadsPerStep = (kSlots + kLoadSteps - 1) / kLoadSteps;
   const int nks = p.k_stages;   // 0 when K = 0: C is written as zeros
 

@@ -19,8 +19,8 @@ struct TypeBF16 {
   using x8 = bf16x8;
 };
 
-// A row whose largest magnitude is below this counts as zero: 127 / a then
-// stays finite.
+// A row whose largest magnitude is below this counts as zero: 127 (1 / a)
+// then stays finite.
 constexpr float kTinyRow = 0x1p-100f;
 constexpr uint32_t kInfBits = 0x7F800000u;
 
@@ -42,7 +42,7 @@ __device__ __forceinline__ uint32_t magnitude_bits(float z) {
   return __builtin_bit_cast(uint32_t, z) & 0x7FFFFFFFu;
 }
 
-// Eight codes RNE(z inv) of values with |z inv| <= 127 (1 + 2^-23): adding
+// Eight codes RNE(z inv) of values with |z inv| <= 127 (1 + 2^-22): adding
 // 1.5 * 2^23 rounds the product to an integer and leaves its two's
 // complement in the low byte of the sum.  The product is rounded to binary32
 // before that, as the codes' definition says: no fused multiply-add here.
@@ -130,7 +130,7 @@ __device__ __forceinline__ void row_factors(uint32_t amax_bits, float sumsq, con
   } else if (a < kTinyRow) {
     scale = 0.f;
   } else {
-    inv = __fdiv_rn(127.f, a);
+    inv = __fmul_rn(127.f, __fdiv_rn(1.f, a));
     scale = __fdiv_rn(a, 127.f);
     if (NORM)
       scale = __fmul_rn(scale, __fdiv_rn(1.f, __fsqrt_rn(__fadd_rn(__fdiv_rn(sumsq, (float)p.K), p.eps))));

@@ -14,14 +14,14 @@ def to64(t):
 
 def rows_int8(z32):
     """Codes and a (the largest magnitude) of binary32 rows z, by the rule
-    q = rne(z * (127 / a)) in binary32; rows with a < 2^-100 or a non-finite
+    q = rne(z * (127 * (1 / a))), each operation in binary32; rows with a < 2^-100 or a non-finite
     value get codes 0."""
     assert z32.dtype == np.float32
     a = np.abs(z32).max(axis=1, initial=0.0).astype(np.float32)
     finite = np.isfinite(z32).all(axis=1)
     live = finite & (a >= np.float32(TINY))
     with np.errstate(all="ignore"):
-        inv = np.where(live, np.float32(127) / a, np.float32(0)).astype(np.float32)
+        inv = np.where(live, np.float32(127) * (np.float32(1) / a), np.float32(0)).astype(np.float32)
         q = np.rint((z32 * inv[:, None]).astype(np.float32))
     q[~live] = 0
     return q.astype(np.int8), a, live, finite
