@@ -44,68 +44,84 @@ inline int64_t grouped_max_tiles(int64_t rows, int64_t groups, int tile) {
 // The kernel for the sizes.  How the rows fall on the groups is known on the
 // device only; the choice goes by the mean, and by how many tiles the rows
 // would make if half the groups ended in a tile of their own (and most had
-// one).  Measured at
-// 250 sizes of one group (1 to 4096 rows) and of 8 to 128 groups (1 to 2048
-// tokens, 2 or 8 experts each), N = 768 to 14336, K = 2048 to 14336 (graph
-// replay, one MI355X; the figures at each rule are us with the kernel it
-// takes against the next best).
+// one).  Measured with every kernel at 2016 sizes: one group of 1 to 6000
+// rows, and 4 to 128 groups of 1 to 600 rows each on average, evenly and
+// unevenly spread, N = 512 to 14336, K = 1024 to 7168, with weights that are
+// in no cache (graph replay, one MI355X).  At 756 other sizes the choice is 3%
+// (int8), 2% (binary16, MXFP4 experts) and 1% (one group) behind the best
+// kernel of each in the geometric mean, a tenth of them by 12, 9, 8 and 3% or
+// more, the worst 1.6 times.  The figures at each rule are us of the kernel it
+// takes against another, or of both where it turns.
 inline GroupedCfg choose_grouped(int kind, int64_t rows, int64_t groups, int64_t N, int64_t row_bytes, int cu_count) {
   const int64_t used = groups < rows ? groups : rows;
   const int64_t mean = (rows + used - 1) / used;
-  // tiles of a configuration, and whether they reach `percent` of the CUs
-  auto fills = [&](GroupedCfg c, int64_t percent) {
+  const bool one = used == 1, f16 = kind == KIND_F16, mxfp4 = kind == KIND_MXFP4;
+  // workgroups of a configuration, and whether they reach `percent` of the CUs
+  auto grid = [&](GroupedCfg c) {
     const int64_t ragged = rows / grouped_tile_rows(c) + (used + 1) / 2, most = (4 * used + 4) / 5;
-    const int64_t t = used == 1 ? tiles(rows, grouped_tile_rows(c)) : ragged > most ? ragged : most;
-    return 100 * t * tiles(N, grouped_tile_cols(c)) >= percent * cu_count;
+    const int64_t t = one ? tiles(rows, grouped_tile_rows(c)) : ragged > most ? ragged : most;
+    return t * tiles(N, grouped_tile_cols(c));
   };
+  auto fills = [&](GroupedCfg c, int64_t percent) { return 100 * grid(c) >= percent * cu_count; };
+  // percent of a round of `slots` workgroups; the first four rounds count whole
+  auto rounds = [](int64_t t, int64_t slots) { return t <= 4 * slots ? 100 * ((t + slots - 1) / slots) : 100 * t / slots; };
   // MXFP4 experts whose weights are more than the 256 MiB Infinity Cache keeps
   // from one call to the next, and mostly read by one row tile: B streams
-  // non-temporally (64 experts of 2048 x 4096: 24 rows each 56.2 against 61.8
-  // us, 12 rows 50.8 against 54.4; 128 of 1024 x 2048, 24 rows 35.4 against
-  // 37.2; at 67 MB of weights 1.3-1.4 times slower, and with rows that do not
-  // start on a cache line 1.25 times: each line is fetched twice)
-  if (kind == KIND_MXFP4 && used > 1 && row_bytes % 128 == 0 && groups * N * row_bytes >= (int64_t)100 << 20) {
+  // non-temporally (64 experts of 2048 x 4096, 10 rows each 52.9 against 58.6
+  // us; 128 of 4096 x 4096, 4 rows each 191 against 207; with weights of 67 MB
+  // that stay cached 1.3-1.4 times slower, with rows that do not start on a
+  // cache line 1.25 times: each line is fetched twice; at K = 1024, four
+  // lines a row, no faster: 64 of 7168 x 1024 26.6 against 25.6)
+  if (mxfp4 && !one && row_bytes % 128 == 0 && row_bytes > 512 && groups * N * row_bytes >= (int64_t)100 << 20) {
     if (mean > 16 && mean < 96) return GCFG_128x128_NT;
     if (mean > 4 && mean <= 16) return GCFG_64x64_NT;
   }
   // few rows per group: the weights' stream is the work, and narrow tiles
-  // whose waves split K keep most of it in flight (int8, 8 tokens over 64
-  // experts of 2048 x 2048: 22.9 against 25.4 us on 64 x 64 tiles; MXFP4,
-  // 16 rows of 14336 x 4096: 8.9 against 10.3).  With several groups up to 12
-  // rows each (64 groups of 16 rows: int8 51.7 on 64 x 64 tiles against 65.7);
-  // MXFP4, half the bytes per row, up to 6 (8 rows: 31.4 against 34.8);
-  // binary16, twice as many, up to 16 (16 rows: 103 against 104 and more).
-  const bool few = used == 1 ? mean <= 16 : mean <= (kind == KIND_MXFP4 ? 6 : kind == KIND_F16 ? 16 : 12);
-  if (!few) {
-    // 256 x 256 tiles move the fewest bytes per product, but leave a ragged
-    // group's last tile emptier (MXFP4 4096 x 4096 x 4096: 46.5 us against
-    // 53.5 on 128 x 128; 8 groups of 512 rows, N = 14336: 227 against 231, at
-    // N = 4096 59.5 against 44.4)
-    if (used == 1 ? fills(GCFG_256x256, 60) : mean >= 256 && fills(GCFG_256x256, 250)) return GCFG_256x256;
+  // whose waves split K keep most of it in flight.  One group up to 20 rows
+  // (MXFP4 18 x 7168 x 4096: 6.4 against 8.9 on 64 x 64 tiles; 36 x 14336 x
+  // 7168: 26.8 against 14.6).  Several, int8, up to 12 rows each (31 groups of
+  // 12, 1416 x 4096: 34.4 against 43.6; of 15, 2048 x 1024: 23.2 against
+  // 17.4); binary16, twice the bytes, up to 20 (31 groups of 19, 2048 x 2048:
+  // 49.3 against 60.0; of 32, 7168 x 1024: 142 against 92); MXFP4, half the
+  // bytes, up to 10, and where eight stages or fewer leave a wave two, only
+  // while there are few workgroups (31 groups of 7, 7168 x 1024: 41.0 against
+  // 33.2; one row, 2048 x 1024: 5.9 against 7.1)
+  const int64_t limit = one || f16 ? 20 : mxfp4 ? 10 : 12;
+  const bool shallow = mxfp4 && !one && row_bytes <= 1024 && fills(GCFG_64x64_S2, 150);
+  if (mean > limit || shallow) {
+    // 256 x 256 tiles, one workgroup on a CU, or 128 x 128, two: a round of the
+    // former takes 1.6 rounds of the latter (MXFP4, 288 tiles in two rounds of
+    // 256, 4357 x 4096 x 2048: 33.0 on 128 x 128 against 41.3; 176 in one,
+    // 2697 x 4096 x 4096: 32.5 on 256 x 256 against 40.6; int8, 16 groups of
+    // 350 rows, 2048 x 4096: 256 x 256 is 1.3 times faster)
+    if ((one || mean >= 96) && 160 * rounds(grid(GCFG_256x256), cu_count) <= 100 * rounds(grid(GCFG_128x128), 2 * cu_count))
+      return GCFG_256x256;
     // two workgroups of 128 x 128 tiles share a CU: one's stores and first
-    // loads behind the other's products (MXFP4 2048 x 4096 x 4096 28.1 against
-    // 34.8 on 64 x 128; 3000 x 1536 x 3584 18.7 against 25.5; 1024 x 4096 x
-    // 4096, one tile per CU, 20.6 against 19.4)
-    if (mean >= 48 && fills(GCFG_128x128, 105)) return GCFG_128x128;
-    // int8, 64 groups of 64 rows: 73.9 against 79.1 on 128 x 128 tiles; MXFP4
-    // 256 x 14336 x 4096: 19.2 against 20.1; binary16, whose stage holds half
-    // the k, keeps the deeper ring below 96 rows (64 groups of 25 rows, N =
-    // 1500: 87.9 against 110)
-    const bool f16 = kind == KIND_F16;
-    if (mean >= (f16 ? 96 : 24) && fills(GCFG_64x128, 150)) return GCFG_64x128;
-    // up to two tiles per CU: the deeper ring (MXFP4 512 x 4096 x 14336 34.1
-    // against 37.9); beyond that: more workgroups (8 groups of 64 rows, N =
-    // 4096: 12.9 against 16.3)
+    // loads behind the other's products (MXFP4 1280 x 14336 x 4096: 60.3
+    // against 80.1 on 64 x 128; int8, 16 groups of 143 rows, 2048 x 4096: 46.6
+    // against 51.9; less than a tile per CU, MXFP4 677 x 4096 x 4096: 19.2
+    // against 17.5)
+    if (mean >= (one ? 48 : 32) && fills(GCFG_128x128, one ? 105 : 130)) return GCFG_128x128;
+    // (MXFP4 788 x 4096 x 7168: 28.6 against 31.6 on 64 x 64 tiles; binary16,
+    // whose stage holds half the k, keeps the deeper ring of 64 x 64 at few
+    // rows: 64 groups of 24, 2048 x 2048: 111 against 140)
+    if (mean >= (f16 ? 32 : 24) && fills(GCFG_64x128, 150)) return GCFG_64x128;
+    // up to two tiles per CU: the deeper ring (MXFP4 181 x 7168 x 4096: 14.0
+    // against 16.7); beyond that: more workgroups (677 x 4096 x 4096: 17.5
+    // against 20.1)
     if (!f16 && fills(GCFG_64x64_S2, 201)) return GCFG_64x64_S2;
-    if (fills(GCFG_64x64_S4, 60)) return GCFG_64x64_S4;
+    if (fills(GCFG_64x64_S4, one || mean >= 48 ? 45 : 60)) return GCFG_64x64_S4;
   }
   // the lowest tile that keeps the workgroups near one per CU, up to what the
-  // rows need (MXFP4 16 x 4096 x 4096: 8 rows 5.2 us, 16 rows 6.0; 32 rows
-  // there: 8 rows 6.6, 16 rows 5.9; 64 rows: 32 rows 6.6, 16 rows 7.4)
-  if (used == 1 ? mean <= 8 || !fills(GCFG_SKINNY_8, 126) : mean <= (kind == KIND_F16 ? 2 : 4))
-    return fills(GCFG_SKINNY_8, 201) ? GCFG_SKINNY_8 : GCFG_SKINNY_8_DEEP;
-  if (used == 1 ? mean <= 16 || !fills(GCFG_SKINNY_16, 126) : mean <= (kind == KIND_F16 ? 8 : 12))
-    return GCFG_SKINNY_16;
+  // rows need (MXFP4 37 x 1024 x 4096: 8 rows 4.2, 32 rows 5.3; 45 x 4096 x
+  // 4096: 32 rows 6.0, 8 rows 7.9); with several groups by their mean rows
+  // (int8, 31 groups of 12, 1416 x 4096: 16 rows 34.4, 32 rows 36.6, 8 rows
+  // 42.3; MXFP4, 64 of 1 or 2, 2048 x 4096: 8 rows 47.0, 16 rows 46.5).  Ring
+  // of 2 blocks from two workgroups a CU on (MXFP4, 9 experts of one row, 2048
+  // x 1024: 5.9 against 7.3 with 3; at K = 4096 10.0 against 9.5)
+  if (mean <= (one ? 8 : f16 || mxfp4 ? 4 : 6) || !fills(GCFG_SKINNY_8, 101))
+    return fills(GCFG_SKINNY_8, mxfp4 && !one ? 150 : 201) ? GCFG_SKINNY_8 : GCFG_SKINNY_8_DEEP;
+  if (mean <= (one ? 16 : 12) || !fills(GCFG_SKINNY_16, 101)) return GCFG_SKINNY_16;
   return GCFG_SKINNY_32;
 }
 

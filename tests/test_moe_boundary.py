@@ -163,16 +163,20 @@ def test_grouped_configs():
         ("mxfp4", 3000, 1, 1536, 7), ("mxfp4", 2048, 1, 4096, 7), ("mxfp4", 4096, 1, 4096, 8), ("mxfp4", 8192, 1, 8192, 8),
         # experts: by the mean of their rows
         ("i8", 8, 64, 2048, 0), ("i8", 64, 64, 2048, 1), ("i8", 512, 64, 2048, 2), ("i8", 1024, 64, 2048, 5),
-        ("i8", 2048, 64, 2048, 6), ("i8", 4096, 64, 2048, 7), ("i8", 8192, 8, 14336, 8), ("i8", 60, 4, 2048, 3),
-        ("mxfp4", 512, 64, 2048, 5), ("mxfp4", 256, 64, 2048, 1), ("mxfp4", 300, 64, 2048, 2),
-        ("f16", 1000, 64, 2048, 3), ("f16", 500, 64, 2048, 2), ("f16", 2048, 64, 2048, 4), ("f16", 6400, 64, 1500, 7),
+        ("i8", 2048, 64, 2048, 7), ("i8", 4096, 64, 2048, 7), ("i8", 8192, 8, 14336, 8), ("i8", 60, 4, 2048, 3),
+        ("mxfp4", 512, 64, 2048, 5), ("mxfp4", 256, 64, 2048, 5), ("mxfp4", 300, 64, 2048, 5), ("mxfp4", 10, 31, 2048, 1),
+        ("f16", 1000, 64, 2048, 3), ("f16", 500, 64, 2048, 2), ("f16", 2048, 64, 2048, 7), ("f16", 1536, 64, 2048, 4), ("f16", 6400, 64, 1500, 7),
     ]
     got = [(*r[:4], lp.grouped_auto_config(*r[:4], 1024, 256)) for r in rules]
     assert got == rules
     # MXFP4 experts of more than 100 MiB, rows on cache lines: streamed
     for rows, K, config in ((256, 4096, 1), (512, 4096, 9), (1024, 4096, 9), (2048, 4096, 10), (5000, 4096, 10),
-                            (6200, 4096, 7), (2048, 4128, 6), (2048, 1024, 6)):
+                            (6200, 4096, 7), (2048, 4128, 7), (2048, 1024, 7)):
         assert lp.grouped_auto_config("mxfp4", rows, 64, 2048, K, 256) == config, (rows, K)
+    # whole rounds of 256 x 256 tiles (one a CU) against rounds of 128 x 128 (two)
+    for kind, rows, groups, N, config in (("mxfp4", 2697, 1, 4096, 8), ("mxfp4", 4357, 1, 4096, 7), ("mxfp4", 677, 1, 4096, 5),
+                                          ("i8", 5600, 16, 2048, 8), ("i8", 2300, 16, 2048, 7)):
+        assert lp.grouped_auto_config(kind, rows, groups, N, 4096, 256) == config, (kind, rows)
     for bad in (("i8", 0, 1, 1, 16, 256), ("i8", 1, 0, 1, 16, 256), ("i8", 1, 1, 0, 16, 256), ("i8", 1, 1, 1, -1, 256),
                 ("i8", 1, 1, 1, 16, 0), ("i8", 2 ** 31, 1, 1, 16, 256)):
         assert lp.grouped_auto_config(*bad) == -1
