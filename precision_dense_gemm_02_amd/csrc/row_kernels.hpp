@@ -164,7 +164,16 @@ __device__ __forceinline__ void row_join(uint32_t& amax, float& sumsq, int wave)
 // a row and each lane keeps its NC chunks of 8 values (chunk li + 64 WPR c).
 // Chunks past the row's end load as zero through the buffer resource, which
 // changes neither the maximum nor the sum of squares.  All loads of a row go
-// out before the first is used.
+// out before the first is used: of one row with WPR > 1, of one per wave
+// otherwise.
+//
+// Bound by HBM from a few hundred rows on (norm 7, activation 5 bytes a value;
+// bfloat16, inputs in no cache: norm of 8192 x 8192 83.5 us, 5.6 TB/s; the
+// activation of 4096 x 14336 55.1, 5.3 TB/s), below that by the launch and a
+// trip to memory (1 x 4096 2.7 us, 16 x 14336 4.1).  Non-temporal stores would
+// take 2 to 5% off the large ones and slow the product that reads the codes
+// by more (activation of 4096 x 14336 and the product with 4096 columns 249
+// against 234 us; 1024 rows 116 against 118).
 template <typename T, bool NORM, int WPR, int NC>
 __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void rows_int8_regs(RowArgs p) {
   constexpr int kRowLanes = 64 * WPR;
@@ -233,7 +242,8 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void rows_int8_regs(RowA
 }
 
 // Longer rows (and K = 0): a workgroup per row and two passes over it, the
-// second mostly from the L2.  A thread handles the same chunks in both, so
+// second mostly from the L2 (norm of 4096 x 40000 249 us, 4.6 TB/s; activation
+// of 2048 x 40000 114, 3.6 TB/s).  A thread handles the same chunks in both, so
 // the second may read back an H that overwrote X or R.
 template <typename T, bool NORM>
 __global__ __launch_bounds__(1024) void rows_int8_long(RowArgs p) {
@@ -290,13 +300,9 @@ struct Mxfp4Args {
   uint32_t total;        // rows x chunks of this launch
 };
 
+// One block of a row by the four lanes that hold its values v, at chunk c.
 template <typename T>
-__global__ __launch_bounds__(256) void quantize_mxfp4_kernel(Mxfp4Args p) {
-  const uint32_t idx = blockIdx.x * 256u + threadIdx.x;
-  const bool on = idx < p.total;   // a block's four lanes are on together: chunks is a multiple of 4
-  const uint32_t row = on ? idx / (uint32_t)p.chunks : 0, c = on ? idx - row * (uint32_t)p.chunks : 0;
-  i32x4 v = {0, 0, 0, 0};
-  if (on) v = *(const i32x4*)(p.X + (int64_t)row * p.x_stride + (int64_t)c * 16);
+__device__ __forceinline__ void quantize_chunk(const Mxfp4Args& p, i32x4 v, uint32_t row, uint32_t c, bool on) {
   f32x8 x = widen<T>(v);
   uint32_t amax = 0;
 #pragma unroll
@@ -330,8 +336,35 @@ __global__ __launch_bounds__(256) void quantize_mxfp4_kernel(Mxfp4Args p) {
   }
 }
 
-// Eight values per lane: code times 2^(b - 127), in binary32, rounded to the
-// output's type (OUT: 0 binary32, 1 binary16, 2 bfloat16).
+// UNROLL chunks per lane, 256 apart, all loaded before the first is used.
+// HBM-bound: 2 + 17/32 bytes a value (bfloat16, inputs in no cache: 14336 x
+// 4096 29.8 us, 5.0 TB/s; 33 x 4096 2.0).  Non-temporal loads: 97 against 104
+// at 32768 x 7168, but 36.1 against 35.6 at 8192 x 4096 where the values were
+// just written.
+template <typename T, int UNROLL>
+__global__ __launch_bounds__(256) void quantize_mxfp4_kernel(Mxfp4Args p) {
+  i32x4 v[UNROLL];
+  uint32_t row[UNROLL], c[UNROLL];
+  bool on[UNROLL];   // a block's four lanes are on together: chunks is a multiple of 4
+#pragma unroll
+  for (int u = 0; u < UNROLL; ++u) {
+    const uint32_t idx = (blockIdx.x * UNROLL + u) * 256u + threadIdx.x;
+    on[u] = idx < p.total;
+    row[u] = on[u] ? idx / (uint32_t)p.chunks : 0;
+    c[u] = on[u] ? idx - row[u] * (uint32_t)p.chunks : 0;
+    v[u] = i32x4{0, 0, 0, 0};
+    if (on[u]) v[u] = *(const i32x4*)(p.X + (int64_t)row[u] * p.x_stride + (int64_t)c[u] * 16);
+  }
+#pragma unroll
+  for (int u = 0; u < UNROLL; ++u) quantize_chunk<T>(p, v[u], row[u], c[u], on[u]);
+}
+
+// Eight values per lane and chunk: code times 2^(b - 127), in binary32, rounded
+// to the output's type (OUT: 0 binary32, 1 binary16, 2 bfloat16); UNROLL
+// chunks, 256 apart.  Bound by its stores (to bfloat16, 14336 x 4096, in no cache: 29.8 us, 5.0 TB/s).
+// Non-temporal ones are faster alone (4096 x 4096 9.4 against 10.5 us) and
+// slow down whoever reads the values next (with a product of 64 rows behind
+// it 35.1 against 31.9).
 struct Dequant4Args {
   const uint8_t* codes;
   const uint8_t* scales;
@@ -341,30 +374,42 @@ struct Dequant4Args {
   uint32_t total;
 };
 
-template <int OUT>
+template <int OUT, int UNROLL>
 __global__ __launch_bounds__(256) void dequantize_mxfp4_kernel(Dequant4Args p) {
-  const uint32_t idx = blockIdx.x * 256u + threadIdx.x;
-  if (idx >= p.total) return;
-  const uint32_t row = idx / (uint32_t)p.chunks, c = idx - row * (uint32_t)p.chunks;
-  const uint32_t code = *(const uint32_t*)(p.codes + (int64_t)idx * 4);
-  const uint32_t b = p.scales[(int64_t)row * p.scale_stride + (c >> 2)];
-  // 2^(b - 127); b = 0 is a subnormal, 255 a NaN
-  const float unit = __builtin_bit_cast(float, b == 255 ? 0x7FC00000u : (b == 0 ? 0x00400000u : b << 23));
-  typedef float f32x2_t __attribute__((ext_vector_type(2)));
-  const f32x2_t v0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, 1.f, 0);
-  const f32x2_t v1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, 1.f, 1);
-  const f32x2_t v2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, 1.f, 2);
-  const f32x2_t v3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, 1.f, 3);
-  f32x8 y = {v0.x, v0.y, v1.x, v1.y, v2.x, v2.y, v3.x, v3.y};
+  uint32_t codes[UNROLL], bytes[UNROLL];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) y[e] *= unit;
-  if constexpr (OUT == 0) {
-    f32x8* const out = (f32x8*)(p.Y + (int64_t)idx * 32);
-    *out = y;
-  } else if constexpr (OUT == 1) {
-    *(i32x4*)(p.Y + (int64_t)idx * 16) = narrow<TypeF16>(y);
-  } else {
-    *(i32x4*)(p.Y + (int64_t)idx * 16) = narrow<TypeBF16>(y);
+  for (int u = 0; u < UNROLL; ++u) {
+    const uint32_t idx = (blockIdx.x * UNROLL + u) * 256u + threadIdx.x;
+    codes[u] = bytes[u] = 0;
+    if (idx < p.total) {
+      const uint32_t row = idx / (uint32_t)p.chunks, c = idx - row * (uint32_t)p.chunks;
+      codes[u] = *(const uint32_t*)(p.codes + (int64_t)idx * 4);
+      bytes[u] = p.scales[(int64_t)row * p.scale_stride + (c >> 2)];
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < UNROLL; ++u) {
+    const uint32_t idx = (blockIdx.x * UNROLL + u) * 256u + threadIdx.x;
+    if (idx >= p.total) return;
+    const uint32_t code = codes[u], b = bytes[u];
+    // 2^(b - 127); b = 0 is a subnormal, 255 a NaN
+    const float unit = __builtin_bit_cast(float, b == 255 ? 0x7FC00000u : (b == 0 ? 0x00400000u : b << 23));
+    typedef float f32x2_t __attribute__((ext_vector_type(2)));
+    const f32x2_t v0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, 1.f, 0);
+    const f32x2_t v1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, 1.f, 1);
+    const f32x2_t v2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, 1.f, 2);
+    const f32x2_t v3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, 1.f, 3);
+    f32x8 y = {v0.x, v0.y, v1.x, v1.y, v2.x, v2.y, v3.x, v3.y};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] *= unit;
+    if constexpr (OUT == 0) {
+      f32x8* const out = (f32x8*)(p.Y + (int64_t)idx * 32);
+      *out = y;
+    } else if constexpr (OUT == 1) {
+      *(i32x4*)(p.Y + (int64_t)idx * 16) = narrow<TypeF16>(y);
+    } else {
+      *(i32x4*)(p.Y + (int64_t)idx * 16) = narrow<TypeBF16>(y);
+    }
   }
 }
 

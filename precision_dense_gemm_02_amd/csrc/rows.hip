@@ -18,28 +18,29 @@ lpgemm_status enqueue(const void* fn, int64_t grid, int threads, void* args, hip
              : LPGEMM_ERROR_LAUNCH;
 }
 
-// The kernel for M rows of K values: in registers up to 16384 values, a
-// wavefront per row once the rows fill the SIMDs (up to 8192 values), else a
-// workgroup per row.
+// The kernel for rows of K values: in registers up to 32768 values, with the
+// wavefronts per row that leave a lane one to four chunks.  More of them lose
+// to the join and to idle lanes, fewer to the latency of a lane's loads
+// (bfloat16, us on one MI355X with 1, 2, 4, 8 and 16 wavefronts; norm, 8192
+// rows of 512: 9.7 10.8 14.8 23.5 45.3; of 1024: 15.1 15.6 18.5 27.0 49.8; of
+// 4096: 50.2 46.8 44.5 46.1 60.4; of 8192: - 89.2 86.0 84.6 90.3; of 14336: -
+// - 148 146 146; activation, 8192 rows of 14336: - - 113 113 106; 16 rows: - -
+// 4.7 4.0 4.0; 8192 rows of 32768: - - - 243 238, and 349 in two passes).
 template <typename T, bool NORM>
-lpgemm_status launch_rows(RowArgs& p, int cu_count, hipStream_t stream) {
+lpgemm_status launch_rows(RowArgs& p, hipStream_t stream) {
   const int K = p.K;
-  if (K == 0 || K > 16384) return enqueue((const void*)&rows_int8_long<T, NORM>, p.M, 1024, &p, stream);
-  const bool wide = p.M < 4 * (int64_t)cu_count || K > 8192;
-  const int nc = (K / 8 + (wide ? 255 : 63)) / (wide ? 256 : 64);
   const void* fn;
-  if (wide)
-    fn = nc <= 1   ? (const void*)&rows_int8_regs<T, NORM, 4, 1>
-         : nc <= 2 ? (const void*)&rows_int8_regs<T, NORM, 4, 2>
-         : nc <= 4 ? (const void*)&rows_int8_regs<T, NORM, 4, 4>
-                   : (const void*)&rows_int8_regs<T, NORM, 4, 8>;
-  else
-    fn = nc <= 1   ? (const void*)&rows_int8_regs<T, NORM, 1, 1>
-         : nc <= 2 ? (const void*)&rows_int8_regs<T, NORM, 1, 2>
-         : nc <= 4 ? (const void*)&rows_int8_regs<T, NORM, 1, 4>
-         : nc <= 8 ? (const void*)&rows_int8_regs<T, NORM, 1, 8>
-                   : (const void*)&rows_int8_regs<T, NORM, 1, 16>;
-  return enqueue(fn, wide ? p.M : ((int64_t)p.M + 3) / 4, 256, &p, stream);
+  int waves, rows = 1;   // wavefronts of a workgroup, its rows
+  if (K == 0 || K > 32768) fn = (const void*)&rows_int8_long<T, NORM>, waves = 16;
+  else if (K <= 512) fn = (const void*)&rows_int8_regs<T, NORM, 1, 1>, waves = rows = 4;
+  else if (K <= 1024) fn = (const void*)&rows_int8_regs<T, NORM, 2, 1>, waves = 2;
+  else if (K <= 2048) fn = (const void*)&rows_int8_regs<T, NORM, 4, 1>, waves = 4;
+  else if (K <= 4096) fn = (const void*)&rows_int8_regs<T, NORM, 4, 2>, waves = 4;
+  else if (K <= 8192) fn = (const void*)&rows_int8_regs<T, NORM, 8, 2>, waves = 8;
+  else if (K <= 16384 && NORM) fn = (const void*)&rows_int8_regs<T, NORM, 8, 4>, waves = 8;
+  else if (K <= 16384) fn = (const void*)&rows_int8_regs<T, NORM, 16, 2>, waves = 16;
+  else fn = (const void*)&rows_int8_regs<T, NORM, 16, 4>, waves = 16;
+  return enqueue(fn, ((int64_t)p.M + rows - 1) / rows, 64 * waves, &p, stream);
 }
 
 // A grid holds less than 2^32 threads: more rows than this go out in several
@@ -47,11 +48,11 @@ lpgemm_status launch_rows(RowArgs& p, int cu_count, hipStream_t stream) {
 constexpr int64_t kRowsPerLaunch = (int64_t)1 << 21;
 
 template <typename T, bool NORM>
-lpgemm_status run_rows(RowArgs p, int64_t M, int cu_count, hipStream_t stream) {
+lpgemm_status run_rows(RowArgs p, int64_t M, hipStream_t stream) {
   lpgemm_status st = LPGEMM_SUCCESS;
   for (int64_t r = 0; r < M && st == LPGEMM_SUCCESS; r += kRowsPerLaunch) {
     p.M = (int)(M - r < kRowsPerLaunch ? M - r : kRowsPerLaunch);
-    st = launch_rows<T, NORM>(p, cu_count, stream);
+    st = launch_rows<T, NORM>(p, stream);
     p.X += kRowsPerLaunch * p.x_stride;
     if (p.R) p.R += kRowsPerLaunch * p.r_stride;
     if (p.H) p.H += kRowsPerLaunch * p.h_stride;
@@ -79,7 +80,7 @@ lpgemm_status lpgemm_add_rmsnorm_quantize(int64_t M, int64_t K, lpgemm_type type
   if (!aligned4(row_scale)) return LPGEMM_ERROR_MISALIGNED;
   if (K > 0 && (!aligned16(X) || !aligned16(R) || !aligned16(weight) || !aligned16(H) || !aligned16(Q)))
     return LPGEMM_ERROR_MISALIGNED;
-  DeviceInfo dev;
+  DeviceInfo dev;   // (fails on another GPU than this library is built for)
   const lpgemm_status st = current_device(dev);
   if (st != LPGEMM_SUCCESS) return st;
   RowArgs p{};
@@ -94,8 +95,8 @@ lpgemm_status lpgemm_add_rmsnorm_quantize(int64_t M, int64_t K, lpgemm_type type
   p.h_stride = 2 * h_stride;
   p.K = (int)K;
   p.eps = eps;
-  return type == LPGEMM_F16 ? run_rows<TypeF16, true>(p, M, dev.cu_count, stream)
-                            : run_rows<TypeBF16, true>(p, M, dev.cu_count, stream);
+  return type == LPGEMM_F16 ? run_rows<TypeF16, true>(p, M, stream)
+                            : run_rows<TypeBF16, true>(p, M, stream);
 }
 
 lpgemm_status lpgemm_silu_mul_quantize(int64_t M, int64_t K, lpgemm_type type, const void* X, int64_t x_stride,
@@ -107,7 +108,7 @@ lpgemm_status lpgemm_silu_mul_quantize(int64_t M, int64_t K, lpgemm_type type, c
   if (!row_scale || (K > 0 && (!X || !Q))) return LPGEMM_ERROR_INVALID_VALUE;
   if (!aligned4(row_scale)) return LPGEMM_ERROR_MISALIGNED;
   if (K > 0 && (!aligned16(X) || !aligned16(Q))) return LPGEMM_ERROR_MISALIGNED;
-  DeviceInfo dev;
+  DeviceInfo dev;   // (fails on another GPU than this library is built for)
   const lpgemm_status st = current_device(dev);
   if (st != LPGEMM_SUCCESS) return st;
   RowArgs p{};
@@ -116,13 +117,21 @@ lpgemm_status lpgemm_silu_mul_quantize(int64_t M, int64_t K, lpgemm_type type, c
   p.scale = row_scale;
   p.x_stride = 2 * x_stride;
   p.K = (int)K;
-  return type == LPGEMM_F16 ? run_rows<TypeF16, false>(p, M, dev.cu_count, stream)
-                            : run_rows<TypeBF16, false>(p, M, dev.cu_count, stream);
+  return type == LPGEMM_F16 ? run_rows<TypeF16, false>(p, M, stream)
+                            : run_rows<TypeBF16, false>(p, M, stream);
 }
 
 // The MXFP4 kernels index a launch's chunks of 8 values in 32 bits; more
 // rows than that go out in several launches.
 static int64_t rows_per_launch(int64_t chunks) { return ((int64_t)1 << 31) / chunks; }
+
+// Two chunks of 8 values per lane, for twice the loads in flight, from 2^25
+// values on (from bfloat16 and back, us with one chunk and with two: 14336
+// x 4096 31.3 and 29.8, inverse 40.0 and 30.3; with a kernel that writes the
+// values before or reads them after, 59.5 and 57.5, 68.3 and 59.5; 4096 x 4096
+// 20.9 and 21.5, 20.8 and 23.4).
+static bool two_chunks(int64_t rows, int64_t chunks) { return rows * chunks >= (int64_t)1 << 22; }
+static int64_t tiles_of(int64_t n, int64_t t) { return (n + t - 1) / t; }
 
 lpgemm_status lpgemm_quantize_mxfp4(int64_t rows, int64_t K, lpgemm_type type, const void* X, int64_t x_stride,
                                     uint8_t* codes, uint8_t* scales, hipStream_t stream) {
@@ -134,9 +143,11 @@ lpgemm_status lpgemm_quantize_mxfp4(int64_t rows, int64_t K, lpgemm_type type, c
   DeviceInfo dev;
   lpgemm_status st = current_device(dev);
   if (st != LPGEMM_SUCCESS) return st;
-  const void* fn = type == LPGEMM_F16 ? (const void*)&quantize_mxfp4_kernel<TypeF16>
-                                      : (const void*)&quantize_mxfp4_kernel<TypeBF16>;
   const int64_t chunks = K / 8, stride = LPGEMM_MXFP4_SCALE_STRIDE(K), most = rows_per_launch(chunks);
+  const bool two = two_chunks(rows, chunks);
+  const void* fn = type == LPGEMM_F16
+                       ? (two ? (const void*)&quantize_mxfp4_kernel<TypeF16, 2> : (const void*)&quantize_mxfp4_kernel<TypeF16, 1>)
+                       : (two ? (const void*)&quantize_mxfp4_kernel<TypeBF16, 2> : (const void*)&quantize_mxfp4_kernel<TypeBF16, 1>);
   for (int64_t r = 0; r < rows && st == LPGEMM_SUCCESS; r += most) {
     const int64_t n = rows - r < most ? rows - r : most;
     Mxfp4Args p{};
@@ -147,7 +158,7 @@ lpgemm_status lpgemm_quantize_mxfp4(int64_t rows, int64_t K, lpgemm_type type, c
     p.chunks = (int)chunks;
     p.scale_stride = (int)stride;
     p.total = (uint32_t)(n * chunks);
-    st = enqueue(fn, (n * chunks + 255) / 256, 256, &p, stream);
+    st = enqueue(fn, tiles_of(n * chunks, two ? 512 : 256), 256, &p, stream);
   }
   return st;
 }
@@ -163,10 +174,12 @@ lpgemm_status lpgemm_dequantize_mxfp4(int64_t rows, int64_t K, const uint8_t* co
   DeviceInfo dev;
   lpgemm_status st = current_device(dev);
   if (st != LPGEMM_SUCCESS) return st;
-  const void* fn = type == LPGEMM_F32   ? (const void*)&dequantize_mxfp4_kernel<0>
-                   : type == LPGEMM_F16 ? (const void*)&dequantize_mxfp4_kernel<1>
-                                        : (const void*)&dequantize_mxfp4_kernel<2>;
   const int64_t chunks = K / 8, stride = LPGEMM_MXFP4_SCALE_STRIDE(K), most = rows_per_launch(chunks);
+  const bool two = two_chunks(rows, chunks);
+  const void* fn =
+      type == LPGEMM_F32   ? (two ? (const void*)&dequantize_mxfp4_kernel<0, 2> : (const void*)&dequantize_mxfp4_kernel<0, 1>)
+      : type == LPGEMM_F16 ? (two ? (const void*)&dequantize_mxfp4_kernel<1, 2> : (const void*)&dequantize_mxfp4_kernel<1, 1>)
+                           : (two ? (const void*)&dequantize_mxfp4_kernel<2, 2> : (const void*)&dequantize_mxfp4_kernel<2, 1>);
   const int64_t size = type == LPGEMM_F32 ? 4 : 2;
   for (int64_t r = 0; r < rows && st == LPGEMM_SUCCESS; r += most) {
     const int64_t n = rows - r < most ? rows - r : most;
@@ -177,7 +190,7 @@ lpgemm_status lpgemm_dequantize_mxfp4(int64_t rows, int64_t K, const uint8_t* co
     p.chunks = (int)chunks;
     p.scale_stride = (int)stride;
     p.total = (uint32_t)(n * chunks);
-    st = enqueue(fn, (n * chunks + 255) / 256, 256, &p, stream);
+    st = enqueue(fn, tiles_of(n * chunks, two ? 512 : 256), 256, &p, stream);
   }
   return st;
 }

@@ -203,6 +203,53 @@ def test_silu_mul_strided():
     _check_silu(x, q, s)
 
 
+# on both sides of every change of the number of wavefronts per row and of
+# chunks per lane, and of the register form; more rows than CUs, too
+FORMS = [512, 520, 1024, 1032, 2048, 2056, 4096, 4104, 8192, 8200, 16384, 16392, 32768, 32776]
+
+
+@pytest.mark.parametrize("t", sorted(TYPES))
+@pytest.mark.parametrize("K", FORMS)
+def test_row_forms(K, t):
+    for M in (1, 3, 300):
+        _case("row forms", M, K, t)
+        x, r = _rows(M, K, TYPES[t], 12), _rows(M, K, TYPES[t], 13)
+        w = _rows(1, K, TYPES[t], 3, False)[0]
+        q, s, h = lp.add_rmsnorm_quantize(x.cuda(), w.cuda(), 1e-6, residual=r.cuda())
+        _check_norm(x, r, w, 1e-6, q, s, h)
+        bx = x.cuda()                                   # h over x
+        q, s, h = lp.add_rmsnorm_quantize(bx, w.cuda(), 1e-6, residual=r.cuda(), residual_out=bx)
+        _check_norm(x, r, w, 1e-6, q, s, h)
+        if M > 3:
+            continue
+        x = _rows(M, 2 * K, TYPES[t], 14)
+        q, s = lp.silu_mul_quantize(x.cuda())
+        _check_silu(x, q, s)
+
+
+@pytest.mark.parametrize("K", FORMS)
+def test_row_forms_special_rows(K):
+    """The row's largest value, an infinity or a NaN in any wavefront's part."""
+    _case("row forms special", K)
+    at = sorted({0, 7, 511 % K, 512 % K, K // 2, K - 9, K - 1})
+    x = torch.zeros(3 * len(at) + 1, K, dtype=torch.bfloat16)
+    for i, k in enumerate(at):
+        x[3 * i, k], x[3 * i + 1, k], x[3 * i + 2, k] = 2.0, float("inf"), float("nan")
+    w = torch.ones(K, dtype=torch.bfloat16)
+    for up in (None, torch.ones(K, dtype=torch.bfloat16)):
+        if up is None:
+            q, s, _ = lp.add_rmsnorm_quantize(x.cuda(), w.cuda(), 0.0)
+        else:
+            q, s = lp.silu_mul_quantize(torch.cat([x, up.expand_as(x)], 1).cuda())
+        q, s = q.cpu(), s.cpu()
+        for i, k in enumerate(at):
+            want = torch.zeros(K, dtype=torch.int8)
+            want[k] = 127
+            assert torch.equal(q[3 * i], want) and s[3 * i] > 0
+            assert s[3 * i + 1].isnan() and s[3 * i + 2].isnan() and (q[3 * i + 1:3 * i + 3] == 0).all()
+        assert s[-1] == 0 and (q[-1] == 0).all()
+
+
 # ------------------------------------------------------------------ MXFP4
 
 def _check_mx(x, codes, scales):
@@ -273,3 +320,22 @@ def test_quantize_mxfp4_strided():
     big[:, 24:248] = x.cuda()
     codes, scales = lp.quantize_mxfp4(big[:, 24:248])
     _check_mx(x, codes, scales)
+
+
+@pytest.mark.parametrize("t", sorted(TYPES))
+@pytest.mark.parametrize("M,K", [(4096, 8192), (4105, 8224)])
+def test_mxfp4_many_values(M, K, t):
+    """From 2^25 values on a lane handles two chunks: the same codes, scales
+    and values as a few rows at a time, and the rows at both ends checked."""
+    _case("mx many", M, K, t)
+    x = torch.randn(M, K, device="cuda").to(TYPES[t])
+    codes, scales = lp.quantize_mxfp4(x)
+    for rows in (slice(0, 3), slice(M - 3, M)):
+        _check_mx(x[rows].cpu(), codes[rows], scales[rows])
+    y = {d: lp.dequantize_mxfp4(codes, scales, out_dtype=d) for d in (torch.float32, torch.float16, torch.bfloat16)}
+    for r in range(0, M, 1500):
+        part = slice(r, min(r + 1500, M))
+        c, s = lp.quantize_mxfp4(x[part])
+        assert torch.equal(codes[part], c) and torch.equal(scales[part], s)
+        for d in y:
+            assert torch.equal(y[d][part], lp.dequantize_mxfp4(c, s, out_dtype=d))
