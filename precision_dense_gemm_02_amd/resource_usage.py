@@ -48,6 +48,19 @@ DEFAULT_KERNELS = {
     "lpgemm::gemm_tiled<0, 64, 64, 2, 2>": "int8, small grids (1024^3, 512^3)",
     "lpgemm::quantize_rows_f16_regs<4, 2>": "W8A8 row quantiser, short M",
     "lpgemm::quantize_rows_f16_regs<1, 8>": "W8A8 row quantiser, M = 2048",
+    "lpgemm::rows_int8_regs<lpgemm::TypeBF16, true, 4, 2>": "RMSNorm with int8 rows of 4096",
+    "lpgemm::rows_int8_regs<lpgemm::TypeF16, true, 8, 2>": "RMSNorm with int8 rows of 8192",
+    "lpgemm::rows_int8_regs<lpgemm::TypeBF16, false, 16, 2>": "silu * up with int8 rows of 14336",
+    "lpgemm::quantize_mxfp4_kernel<lpgemm::TypeBF16, 2>": "MXFP4 quantisation, 14336 x 4096",
+    "lpgemm::dequantize_mxfp4_kernel<2, 2>": "MXFP4 values as bfloat16, 14336 x 4096",
+    "lpgemm::grouped_skinny<3, 4, 3, 1>": "int8 experts, one token",
+    "lpgemm::grouped_skinny<6, 4, 2, 2>": "MXFP4, 16 rows of 14336 x 4096",
+    "lpgemm::grouped_tile<6, 64, 64, 2, 2, 4, false, false, false>": "MXFP4, 512 x 4096 x 4096",
+    "lpgemm::grouped_tile<3, 64, 128, 1, 4, 2, false, false, false>": "int8 experts of 32 rows",
+    "lpgemm::grouped_tile<2, 128, 128, 2, 2, 2, false, true, false>": "binary16 experts of 66 rows",
+    "lpgemm::grouped_tile<6, 128, 128, 2, 2, 2, false, true, true>": "MXFP4 experts of 32 rows, B non-temporal",
+    "lpgemm::grouped_tile<3, 256, 256, 2, 2, 2, true, true, false>": "int8 experts of 1024 rows",
+    "lpgemm::grouped_tile<6, 256, 256, 2, 2, 2, true, true, false>": "MXFP4 8192^3",
 }
 FIELDS = ["VGPRs", "AGPRs", "TotalSGPRs", "ScratchSize [bytes/lane]", "LDS Size [bytes/block]",
           "Occupancy [waves/SIMD]", "VGPRs Spill"]
