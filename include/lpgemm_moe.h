@@ -64,6 +64,10 @@ lpgemm_status lpgemm_add_rmsnorm_quantize(int64_t M, int64_t K, lpgemm_type type
  * holds the K gate values g and then the K values u (the layout the product
  * with gate and up weights stacked along N writes); a, Q and the zero and
  * non-finite rows as for lpgemm_add_rmsnorm_quantize, row_scale = a / 127.
+ * z_k is within 8 units of 2^-24 of its exact value, relative (12 for g_k below
+ * -86), so a code may be the neighbour of the correctly rounded one where
+ * z_k * 127 / a lies that near to halfway between two.  Below g_k = -88.72
+ * exp(-g_k) leaves binary32 and z_k is a zero.
  * X: M rows of 2K values of `type`, x_stride >= 2K in elements, a multiple of
  * 8; Q: M x K int8; row_scale: M floats.  K a multiple of 8, at most
  * LPGEMM_MAX_K_QUANT.  Pointers 16-byte aligned, row_scale 4-byte.  M = 0 is

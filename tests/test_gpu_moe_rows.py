@@ -195,6 +195,33 @@ def test_silu_mul_special_rows(t):
     assert s.cpu()[0] == 0 and s.cpu()[3] == 0
 
 
+@pytest.mark.parametrize("t", sorted(TYPES))
+def test_silu_mul_every_gate(t):
+    """Every finite 16-bit gate, alone in its row, against 64 bits.  In units
+    of 2^-24: the exponential 2, its remainder's factor 1, the sum with one 1,
+    the reciprocal 2, two products and the scale's division 1 each: 8, here 9;
+    below -86 the reciprocal is subnormal, 2^-149 in 2^-128, 4 more.  Where
+    exp(-g) leaves binary32 (g < -88.723) the quotient is -0; a largest value
+    below 2^-100 counts as zero, one above binary32 gives NaN."""
+    g = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(TYPES[t])
+    g = g[g.isfinite()]
+    for up in (1.0, 3.0e4, 1e30) if t == "bf16" else (1.0, 65504.0):
+        _case("every gate", t, up)
+        x = torch.zeros(len(g), 16, dtype=TYPES[t])
+        x[:, 0], x[:, 8] = g, up
+        q, s = lp.silu_mul_quantize(x.cuda())
+        q, s = q.cpu(), s.cpu().double()
+        g64 = g.double()
+        z = torch.where(g64 < -88.723, 0.0, g64 / (1 + torch.exp(-g64))) * x[:, 8].double()
+        a = z.abs()
+        zero, past, live = a < ref.TINY * 0.999, a > 3.4029e38, (a > ref.TINY * 1.001) & (a < 3.4027e38)
+        assert (s[zero] == 0).all() and (q[zero] == 0).all()
+        assert s[past].isnan().all() and (q[past] == 0).all()
+        bound = torch.where(g64 < -86, 13.0, 9.0) * ULP
+        assert ((s * 127 - a).abs() <= bound * a)[live].all()
+        assert torch.equal(q[live][:, 0], (127 * torch.sign(z[live])).to(torch.int8))
+
+
 def test_silu_mul_strided():
     x = _rows(33, 2 * 136, torch.bfloat16, 11)
     big = torch.full((33, 2 * 136 + 40), float("nan"), dtype=torch.bfloat16, device="cuda")
