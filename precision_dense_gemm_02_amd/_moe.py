@@ -128,12 +128,12 @@ def _rows(t, name, dtypes):
     if not isinstance(t, _Tensor) or t.dtype not in dtypes or t.dim() != 2 or not t.is_cuda:
         _refuse(t, name, dtypes, dims=2)
     M, K = t.shape
-    if M <= 1 or K == 0:
+    if M == 0 or K == 0:
         return M, K, K
     stride, along = t.stride()
     if along != 1 and K > 1:
         raise ValueError(f"the rows of {name} must be contiguous")
-    return M, K, stride
+    return M, K, stride if M > 1 else K
 
 
 def _out(out, name, shape, dtype, dev):

@@ -150,6 +150,43 @@ def test_binding_refuses_host_tensors_and_types():
         lp.no_such_operator
 
 
+class _OnGpu(torch.Tensor):
+    """A host tensor that says it is on a GPU, for the checks in front of a call."""
+    is_cuda = property(lambda self: True)
+
+
+STRIDED = {
+    "every second column": lambda rows: torch.zeros(rows, 128, dtype=torch.float16)[:, ::2],
+    "a transposed column": lambda rows: torch.zeros(64, 8, dtype=torch.float16)[:, :rows].t(),
+    "one value for a row": lambda rows: torch.zeros(rows, 1, dtype=torch.float16).expand(rows, 64),
+}
+
+
+@pytest.mark.parametrize("view", sorted(STRIDED))
+@pytest.mark.parametrize("rows", [1, 2])
+def test_binding_refuses_columns_that_are_not_adjacent(rows, view):
+    """... in every matrix argument, of one row as of two."""
+    bad = STRIDED[view](rows).as_subclass(_OnGpu)
+    x = torch.zeros(rows, 64, dtype=torch.float16).as_subclass(_OnGpu)
+    w = torch.zeros(64, dtype=torch.float16).as_subclass(_OnGpu)
+    assert bad.shape == x.shape and bad.stride(1) != 1
+    for name, f in (("x", lambda: lp.add_rmsnorm_quantize(bad, w, 1e-6)),
+                    ("residual", lambda: lp.add_rmsnorm_quantize(x, w, 1e-6, residual=bad)),
+                    ("residual_out", lambda: lp.add_rmsnorm_quantize(x, w, 1e-6, residual=x, residual_out=bad)),
+                    ("x", lambda: lp.silu_mul_quantize(bad)), ("x", lambda: lp.quantize_mxfp4(bad))):
+        with pytest.raises(ValueError, match=f"the rows of {name} must be contiguous"):
+            f()
+
+
+def test_row_stride_of_one_row_is_its_length():
+    """The stride from one row to the next has no meaning for a single one."""
+    for t in (torch.zeros(1, 64), torch.zeros(4, 64)[2:3], torch.zeros(64, 1).t(), torch.zeros(4, 100)[1:2, 8:72],
+              torch.zeros(0, 128)[:, ::2]):
+        t = t.half().as_subclass(_OnGpu)
+        assert _moe._rows(t, "x", (torch.float16,)) == (t.shape[0], 64, 64)
+    assert _moe._rows(torch.zeros(4, 100).half()[:, 8:72].as_subclass(_OnGpu), "x", (torch.float16,)) == (4, 64, 100)
+
+
 def test_grouped_configs():
     """The choice by size, pinned where a measured rule changes it (256 CUs)."""
     n = lp.grouped_config_count()
