@@ -540,11 +540,12 @@ __global__ __launch_bounds__(256) void grouped_tile(GroupedArgs p) {
         }
     wait_lgkmcnt0();   // this wave's LDS writes done
     float rs_lane = 0.f;
-    if constexpr (KIND == KIND_I8_DEQUANT) {
-      if (lane < kEpiRows) {
-        const int r = a_row_of(p, row_of(pass, lane), tile.row_end);
-        if (r >= 0) rs_lane = p.row_scale[r];
-      }
+    uint64_t absent = 0;   // rows of the pass that have no row of A, as bits
+    if (KIND == KIND_I8_DEQUANT || gather) {
+      const int row = lane < kEpiRows ? row_of(pass, lane) : tile.row_end;
+      const int r = a_row_of(p, row, tile.row_end);
+      absent = __ballot(r < 0 && row < tile.row_end);
+      if (KIND == KIND_I8_DEQUANT && r >= 0) rs_lane = p.row_scale[r];
     }
     // the staged rows, COLS consecutive columns per lane (16 bytes of C: 4 of
     // binary32, 8 of a 16-bit type)
@@ -594,6 +595,16 @@ __global__ __launch_bounds__(256) void grouped_tile(GroupedArgs p) {
     };
     if (p.out_type == 0) store_rows(std::integral_constant<int, 4>());
     else store_rows(std::integral_constant<int, 8>());
+    // zeros of A times an infinite or NaN weight or scale are not zero: rows
+    // without a row of A are written again, once the stores above are done (a
+    // select in front of every store takes 1 to 2% of the time)
+    if (absent != 0) {
+      wait_vmcnt<0>();
+      for (uint64_t left = absent; left != 0; left &= left - 1) {
+        const size_t idx = (size_t)row_of(pass, __builtin_ctzll(left)) * p.N;
+        for (int col = wcol0 + lane; col < min(wcol0 + WTN, p.N); col += 64) store1(p, idx + col, 0.f);
+      }
+    }
     wait_lgkmcnt0();   // reads done before the next pass overwrites them
   }
 }
@@ -650,6 +661,7 @@ __global__ __launch_bounds__(WAVES * 64) void grouped_skinny(GroupedArgs p) {
   // copy t of a block: rows 8 t + lane / 8, the chunk whose swizzled position
   // is lane % 8
   uint32_t b_off[4], b_col[4], a_off[AG], a_col[AG];
+  uint64_t absent[AG];
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
     const int r = 8 * t + lane / 8;
@@ -662,6 +674,8 @@ __global__ __launch_bounds__(WAVES * 64) void grouped_skinny(GroupedArgs p) {
     const int src = source_row(r);
     a_col[t] = swizzle_chunk(r, lane & 7) * 16;
     a_off[t] = src < 0 ? kOutOfRange : (uint32_t)src * row_bytes + a_col[t];
+    // bit 8 x: row 8 t + x has no row of A
+    absent[t] = __ballot(src < 0);
   }
   // scales: lane l fetches word l % 2 of row l / 2
   uint32_t bs_off = 0, as_off = kOutOfRange;
@@ -755,8 +769,10 @@ __global__ __launch_bounds__(WAVES * 64) void grouped_skinny(GroupedArgs p) {
   __syncthreads();
   const uint32_t* const all = (const uint32_t*)smem;
   const int rows = tile.row_end - tile.row0;
-  for (int x = tid; x < MT * 32; x += WAVES * 64) {
-    const int r = x / 32, c = x % 32;
+  static_assert(WAVES == 4, "each step of the loop below stores 8 rows");
+#pragma unroll
+  for (int t = 0; t < AG; ++t) {
+    const int r = 8 * t + tid / 32, c = tid % 32;
     if (r >= rows || c >= cols) continue;
     float v;
     if constexpr (KIND == KIND_I8_DEQUANT) {
@@ -771,6 +787,8 @@ __global__ __launch_bounds__(WAVES * 64) void grouped_skinny(GroupedArgs p) {
 #pragma unroll
       for (int w = 0; w < WAVES; ++w) v += __builtin_bit_cast(float, all[w * (kWaveLds / 4) + r * kPitch + c]);
     }
+    // (zeros of A times an infinite or NaN weight or scale are not zero)
+    if ((absent[t] >> (8 * (tid / 32))) & 1) v = 0.f;
     store1(p, (size_t)(tile.row0 + r) * p.N + n0 + c, v);
   }
 }

@@ -273,6 +273,39 @@ def test_every_kernel_k_zero_and_untouched_rows(kind, forced):
     test_rows_outside_groups_and_bad_routing(kind, 300, 4)
 
 
+@pytest.mark.parametrize("kind", KINDS)
+def test_every_kernel_rows_without_a_token(kind, forced):
+    """A row_index outside A gives zeros also where the weights or their
+    scales are infinite or NaN; so does a product without tokens."""
+    for counts, N, ksteps in (((3, 1), 33, 3), ((40, 70, 5), 96, 9), ((300,), 130, 8)):
+        K, rows = ksteps * K_STEP[kind], sum(counts)
+        print("[case] no token", forced, kind, counts, N, K, flush=True)
+        p = Problem(kind, 50, len(counts), N, K, seed=rows)
+        bad = np.arange(1, N, 3)
+        if kind == "i8":
+            p.cs[:, bad] = np.array([np.inf, np.nan, -np.inf], dtype=np.float32)[bad % 3]
+        elif kind == "f16":
+            p.b[:, bad, K // 2] = np.array([np.inf, np.nan, -np.inf], dtype=np.float16)[bad % 3]
+        else:
+            p.bs[:, bad, 0] = 255
+        offsets = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+        index = p.rng.integers(0, 50, rows).astype(np.int32)
+        absent = np.unique(np.concatenate([[0, rows - 1], p.rng.integers(0, rows, rows // 3)]))
+        index[absent] = p.rng.choice([-1, 50, -2 ** 31, 2 ** 31 - 1], len(absent))
+        with_token = np.setdiff1d(np.arange(rows), absent)
+        for t in TYPES:
+            c = p.run(offsets, index, t).cpu()
+            assert (c[absent] == 0).all()
+            assert (~c[with_token][:, bad].isfinite()).all()
+            assert c[with_token][:, np.setdiff1d(np.arange(N), bad)].isfinite().all()
+        p.a = p.a[:0]
+        if kind == "i8":
+            p.rs = p.rs[:0]
+        elif kind == "mxfp4":
+            p.as_ = p.as_[:0]
+        assert (p.run(offsets, index) == 0).all()
+
+
 # ------------------------------------------------------------ MXFP4 product
 
 MX_SHAPES = [(1, 1, 32), (1, 33, 64), (16, 70, 4096), (9, 300, 544), (33, 100, 96), (64, 129, 2880), (100, 257, 1024),
