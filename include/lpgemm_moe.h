@@ -47,7 +47,8 @@ typedef enum lpgemm_type {
  * factor cancels out of the codes, which therefore depend on no sum.
  * A row with a below 2^-100 (an all-zero row) gets scale 0 and codes 0.  A
  * row with an infinity or a NaN among its h or z, or whose sum of squares
- * leaves the binary32 range, gets scale NaN and codes 0.
+ * is above the binary32 range, gets scale NaN and codes 0.  Squares that are
+ * too small for binary32 count all the same: eps may be 0.
  * X, R, H: M rows of K values of `type` (LPGEMM_F16 or LPGEMM_BF16), row
  * strides in elements, at least K and multiples of 8 (a stride of an absent
  * R or H is not read); weight: K values of `type`; Q: M x K int8;

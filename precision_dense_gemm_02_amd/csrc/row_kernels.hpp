@@ -14,9 +14,11 @@ typedef float f32x8 __attribute__((ext_vector_type(8)));
 
 struct TypeF16 {
   using x8 = f16x8;
+  static constexpr bool kSquaresUnderflow = false;   // in binary32: the least is 2^-48
 };
 struct TypeBF16 {
   using x8 = bf16x8;
+  static constexpr bool kSquaresUnderflow = true;
 };
 
 // A row whose largest magnitude is below this counts as zero: 127 (1 / a)
@@ -139,11 +141,22 @@ __device__ __forceinline__ f32x8 gated(const i32x4& gate, const i32x4& up) {
   return z;
 }
 
+// Squares of h below 2^-63 are subnormal in binary32 or zero.  That shows in
+// mean h^2 + eps only where both are small: then the sum is taken again, of
+// h 2^100 (at most 2^10 2^-50 2^100 each, and at least 2^-133 2^100).  Rows of
+// ordinary size pay a comparison (us with and without: 8192 x 8192 80.7, 80.5;
+// 4096 x 32768 181.9, 180.2; one row of 4096 2.68, 2.64).
+constexpr int kLift = 100;
+constexpr float kLiftFactor = 0x1p100f;
+__device__ __forceinline__ bool squares_underflow(float sumsq, const RowArgs& p) {
+  return p.eps < 0x1p-100f && sumsq < (float)p.K * 0x1p-100f;
+}
+
 // The scale of a row and the factor of its codes, from the largest magnitude
-// (as bits) and, for the norm, the sum of squares.
+// (as bits) and, for the norm, the sum of squares: of h, or of h 2^kLift.
 template <bool NORM>
 __device__ __forceinline__ void row_factors(uint32_t amax_bits, float sumsq, const RowArgs& p, float& scale,
-                                            float& inv) {
+                                            float& inv, bool lifted = false) {
   const float a = __builtin_bit_cast(float, amax_bits);
   inv = 0.f;
   if (amax_bits >= kInfBits || (NORM && !(sumsq < __builtin_inff()))) {
@@ -153,8 +166,16 @@ __device__ __forceinline__ void row_factors(uint32_t amax_bits, float sumsq, con
   } else {
     inv = __fmul_rn(127.f, __fdiv_rn(1.f, a));
     scale = __fdiv_rn(a, 127.f);
-    if (NORM)
-      scale = __fmul_rn(scale, __fdiv_rn(1.f, __fsqrt_rn(__fadd_rn(__fdiv_rn(sumsq, (float)p.K), p.eps))));
+    if (NORM) {
+      const float eps = lifted ? p.eps * 0x1p100f * 0x1p100f : p.eps;
+      const float rstd = __fdiv_rn(1.f, __fsqrt_rn(__fadd_rn(__fdiv_rn(sumsq, (float)p.K), eps)));
+      if (lifted) {   // rstd is that of h 2^kLift; the exponents meet in integers
+        scale = __builtin_amdgcn_ldexpf(__fmul_rn(__builtin_amdgcn_frexp_mantf(scale), rstd),
+                                        __builtin_amdgcn_frexp_expf(scale) + kLift);
+      } else {
+        scale = __fmul_rn(scale, rstd);
+      }
+    }
   }
 }
 
@@ -179,6 +200,29 @@ __device__ __forceinline__ void row_join(uint32_t& amax, float& sumsq, int wave)
       sumsq += part_sum[i];
     }
   }
+}
+
+// Adds up the waves' second sums (in LDS of its own: the first may still be
+// read).
+template <int WPR>
+__device__ __forceinline__ float row_sum_again(float sumsq, int wave) {
+  sumsq = wave_sum(sumsq);
+  if constexpr (WPR > 1) {
+    __shared__ float part[WPR];
+    if ((threadIdx.x & 63) == 0) part[wave] = sumsq;
+    __syncthreads();
+    sumsq = part[0];
+#pragma unroll
+    for (int i = 1; i < WPR; ++i) sumsq += part[i];
+  }
+  return sumsq;
+}
+template <typename T>
+__device__ __forceinline__ float lifted_squares(const i32x4& h, float sumsq) {
+  const f32x8 f = widen<T>(h);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sumsq = __builtin_fmaf(f[e] * kLiftFactor, f[e] * kLiftFactor, sumsq);
+  return sumsq;
 }
 
 // Rows of at most 512 WPR NC values, held in registers: WPR wavefronts share
@@ -248,8 +292,18 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void rows_int8_regs(RowA
     for (int e = 0; e < 8; ++e) amax = max(amax, magnitude_bits(z[e]));
   }
   row_join<WPR, NORM>(amax, sumsq, wave);
+  bool lifted = false;
+  if constexpr (NORM && T::kSquaresUnderflow) {
+    lifted = squares_underflow(sumsq, p);   // one answer for the row's lanes
+    if (lifted) {
+      sumsq = 0.f;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) sumsq = lifted_squares<T>(x[c], sumsq);
+      sumsq = row_sum_again<WPR>(sumsq, wave);
+    }
+  }
   float scale, inv;
-  row_factors<NORM>(amax, sumsq, p, scale, inv);
+  row_factors<NORM>(amax, sumsq, p, scale, inv, lifted);
   if (li == 0) p.scale[row] = scale;
   uint64_t* const q = (uint64_t*)(p.Q + (int64_t)row * p.K);
 #pragma unroll
@@ -264,8 +318,8 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void rows_int8_regs(RowA
 
 // Longer rows (and K = 0): a workgroup per row and two passes over it, the
 // second mostly from the L2 (norm of 4096 x 40000 249 us, 4.6 TB/s; activation
-// of 2048 x 40000 114, 3.6 TB/s).  A thread handles the same chunks in both, so
-// the second may read back an H that overwrote X or R.
+// of 2048 x 40000 114, 3.6 TB/s).  A thread handles the same chunks in all, so
+// a later one may read back an H that overwrote X or R.
 template <typename T, bool NORM>
 __global__ __launch_bounds__(1024) void rows_int8_long(RowArgs p) {
   const int row = blockIdx.x;
@@ -293,13 +347,25 @@ __global__ __launch_bounds__(1024) void rows_int8_long(RowArgs p) {
     for (int e = 0; e < 8; ++e) amax = max(amax, magnitude_bits(z[e]));
   }
   row_join<16, NORM>(amax, sumsq, wave);
+  // the row's h in the passes after the first: an H that overwrote X or R is
+  // read back
+  auto h_again = [&](int c) { return h ? h[c] : (r ? add_rounded<T>(x[c], r[c]) : x[c]); };
+  bool lifted = false;
+  if constexpr (NORM && T::kSquaresUnderflow) {
+    lifted = squares_underflow(sumsq, p);   // one answer for the row's lanes
+    if (lifted) {
+      sumsq = 0.f;
+      for (int c = threadIdx.x; c < chunks; c += 1024) sumsq = lifted_squares<T>(h_again(c), sumsq);
+      sumsq = row_sum_again<16>(sumsq, wave);
+    }
+  }
   float scale, inv;
-  row_factors<NORM>(amax, sumsq, p, scale, inv);
+  row_factors<NORM>(amax, sumsq, p, scale, inv, lifted);
   if (threadIdx.x == 0) p.scale[row] = scale;
   uint64_t* const q = (uint64_t*)(p.Q + (int64_t)row * p.K);
   for (int c = threadIdx.x; c < chunks; c += 1024) {
     f32x8 z;
-    if constexpr (NORM) z = weighted<T>(h ? h[c] : (r ? add_rounded<T>(x[c], r[c]) : x[c]), w[c]);
+    if constexpr (NORM) z = weighted<T>(h_again(c), w[c]);
     else z = gated<T>(x[c], x[c + chunks]);
     q[c] = inv != 0.f ? int8_codes(z, inv) : 0;
   }

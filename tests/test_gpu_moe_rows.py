@@ -117,6 +117,27 @@ def test_norm_strides_and_in_place(M, K):
         _check_norm(x, r, w, 1e-6, q, s, h)
 
 
+@pytest.mark.parametrize("eps", [0.0, 1e-44, 2.0 ** -110, 1e-25])
+@pytest.mark.parametrize("K", [64, 512, 1024, 2048, 4096, 8192, 16384, 32768, 32776])
+def test_norm_rows_whose_squares_underflow(K, eps):
+    """Rows from 2^-98 up to 2^-40, whose squares are subnormal or zero in
+    binary32, with an eps that does not hide them."""
+    _case("norm underflow", K, eps)
+    g = torch.Generator().manual_seed(K)
+    size = torch.exp2(torch.tensor([-98., -90, -80, -74, -70, -66, -63, -60, -55, -52, -50, -49, -45, -40]))
+    x = (torch.randn(len(size), K, generator=g) * size[:, None]).to(torch.bfloat16)
+    r = (torch.randn(len(size), K, generator=g) * size[:, None]).to(torch.bfloat16)
+    w = _rows(1, K, torch.bfloat16, 3, False)[0]
+    eps = float(np.float32(eps))
+    q, s, h = lp.add_rmsnorm_quantize(x.cuda(), w.cuda(), eps, residual=r.cuda())
+    _check_norm(x, r, w, eps, q, s, h)
+    # large weights on the smallest values
+    w = torch.full((K,), 2.0 ** 60, dtype=torch.bfloat16)
+    x = torch.exp2(torch.randint(-133, -120, (3, K), generator=g).float()).to(torch.bfloat16)
+    q, s, h = lp.add_rmsnorm_quantize(x.cuda(), w.cuda(), eps)
+    _check_norm(x, None, w, eps, q, s, h)
+
+
 def test_norm_rows_past_4_gib():
     """Row offsets past 2^32 bytes, in a stream whose rows lie far apart."""
     M, K, stride = 2200, 512, 1 << 20
