@@ -72,7 +72,9 @@ inline GroupedCfg choose_grouped(int kind, int64_t rows, int64_t groups, int64_t
   // that stay cached 1.3-1.4 times slower, with rows that do not start on a
   // cache line 1.25 times: each line is fetched twice; at K = 1024, four
   // lines a row, no faster: 64 of 7168 x 1024 26.6 against 25.6)
-  if (mxfp4 && !one && row_bytes % 128 == 0 && row_bytes > 512 && groups * N * row_bytes >= (int64_t)100 << 20) {
+  // (divided by the groups: the product of all three may pass 64 bits)
+  const int64_t least = (((int64_t)100 << 20) + groups - 1) / groups;
+  if (mxfp4 && !one && row_bytes % 128 == 0 && row_bytes > 512 && N * row_bytes >= least) {
     if (mean > 16 && mean < 96) return GCFG_128x128_NT;
     if (mean > 4 && mean <= 16) return GCFG_64x64_NT;
   }

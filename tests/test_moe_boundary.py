@@ -217,3 +217,10 @@ def test_grouped_configs():
     for bad in (("i8", 0, 1, 1, 16, 256), ("i8", 1, 0, 1, 16, 256), ("i8", 1, 1, 0, 16, 256), ("i8", 1, 1, 1, -1, 256),
                 ("i8", 1, 1, 1, 16, 0), ("i8", 2 ** 31, 1, 1, 16, 256)):
         assert lp.grouped_auto_config(*bad) == -1
+
+
+def test_grouped_choice_at_the_largest_sizes():
+    """Weights of 2^64 bytes and more are still more than 100 MiB: streamed."""
+    for groups, N, K in ((65536, 2 ** 29, 2 ** 20), (65536, 2 ** 30, 2 ** 20), (2 ** 14, 2 ** 31 - 257, 2 ** 20)):
+        assert lp.grouped_auto_config("mxfp4", 8 * groups, groups, N, K, 256) == 9, (groups, N, K)
+        assert lp.grouped_auto_config("mxfp4", 32 * groups, groups, N, K, 256) == 10, (groups, N, K)
