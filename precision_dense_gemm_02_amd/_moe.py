@@ -17,9 +17,6 @@ from ._binding import LpgemmError, load_library
 
 _i64, _p, _int, _f32 = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_float
 
-MAX_GROUPS = 65536
-MAX_K_MXFP4 = 1048576
-
 _TYPE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 _HALF = {torch.float16: 1, torch.bfloat16: 2}
 _Tensor, _empty = torch.Tensor, torch.empty

@@ -634,6 +634,7 @@ __global__ __launch_bounds__(WAVES * 64) void grouped_skinny(GroupedArgs p) {
   static_assert(WAVES * kWaveLds <= 160 * 1024, "LDS");
   constexpr int kLoads = 4 + AG + (MX ? 2 : 0);   // per block
   static_assert(kLoads * DEPTH <= 63, "vmcnt range");
+  static_assert(DEPTH == 2 || DEPTH == 3, "the waits of the last blocks");
   __shared__ __attribute__((aligned(1024))) uint8_t smem[WAVES * kWaveLds];
 
   const int tid = threadIdx.x;
@@ -745,13 +746,8 @@ __global__ __launch_bounds__(WAVES * 64) void grouped_skinny(GroupedArgs p) {
 #pragma unroll
   for (int left = DEPTH - 1; left >= 1; --left) {
     if (count - i == left) {
-      switch (left) {
-        case 1: wait_vmcnt<0>(); break;
-        case 2: wait_vmcnt<kLoads>(); break;
-        case 3: wait_vmcnt<2 * kLoads>(); break;
-        case 4: wait_vmcnt<3 * kLoads>(); break;
-        default: wait_vmcnt<0>(); break;
-      }
+      if (left == 1) wait_vmcnt<0>();
+      else wait_vmcnt<kLoads>();
       contract(i);
       ++i;
     }
