@@ -365,6 +365,53 @@ def test_mxfp4_empty():
     assert lp.gemm_mxfp4(a, s, a, s).shape == (0, 0)
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 40, 64), (17, 70, 96), (130, 300, 2080), (300, 513, 8192)])
+def test_every_kernel_mxfp4_bit_for_bit(M, N, K, forced):
+    """With one scale for all blocks the products are multiples of a quarter,
+    up to 36, and every partial sum fits 24 bits (36 x 8192 x 4 < 2^24): C is
+    the exact sum, rounded once to its type."""
+    rng = np.random.default_rng(M + K)
+    a, as_ = ref.mx_random(rng, M, K, spread=0)
+    b, bs = ref.mx_random(rng, N, K, spread=0)
+    exact = torch.from_numpy(ref.mx_values(a, as_, K) @ ref.mx_values(b, bs, K).T)
+    offsets = np.array([0, M], dtype=np.int32)
+    for t in TYPES:
+        print("[case] bit for bit", forced, M, N, K, t, flush=True)
+        want = exact.to(TYPES[t])
+        assert torch.equal(lp.gemm_mxfp4(_dev(a), _dev(as_), _dev(b), _dev(bs), out_dtype=TYPES[t]).cpu(), want)
+        assert torch.equal(lp.gemm_mxfp4_grouped(_dev(a), _dev(as_), _dev(b[None]), _dev(bs[None]), _dev(offsets),
+                                                 out_dtype=TYPES[t]).cpu(), want)
+
+
+@pytest.mark.parametrize("sa,sb", [(0, 254), (254, 0), (0, 130), (130, 0), (1, 253), (254, 20)])
+def test_every_kernel_mxfp4_first_and_last_scale(sa, sb, forced):
+    """Scale bytes at both ends, 2^-127 and 2^127, with codes of every value,
+    where the products stay in binary32: exact."""
+    for M, N, K in ((3, 70, 96), (200, 130, 288)):
+        print("[case] scale ends", forced, sa, sb, M, N, K, flush=True)
+        rng = np.random.default_rng(M)
+        a, as_ = ref.mx_random(rng, M, K, spread=0)
+        b, bs = ref.mx_random(rng, N, K, spread=0)
+        as_[:, :K // 32], bs[:, :K // 32] = sa, sb
+        c = ref.to64(lp.gemm_mxfp4(_dev(a), _dev(as_), _dev(b), _dev(bs)))
+        np.testing.assert_array_equal(c, ref.mx_values(a, as_, K) @ ref.mx_values(b, bs, K).T)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("rows,groups", [(700, 5000), (3000, 65536)])
+def test_thousands_of_groups(kind, rows, groups):
+    """Up to the most groups there may be: 1024 scans of 64."""
+    print("[case] thousands of groups", kind, rows, groups, flush=True)
+    K = K_STEP[kind]
+    p = Problem(kind, 30, groups, 9, K, seed=rows)
+    offsets = ref.random_offsets(p.rng, rows, groups)
+    index = p.rng.integers(0, 30, rows).astype(np.int32)
+    p.check(p.run(offsets, index), offsets, index)
+    last = np.zeros(groups + 1, dtype=np.int32)      # all of them in the last group
+    last[-1] = rows
+    p.check(p.run(last, index), last, index)
+
+
 # ------------------------------------------------- streams, graphs, repeats
 
 def test_other_stream_and_graph_replay():
