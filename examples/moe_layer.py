@@ -19,8 +19,12 @@ quantize_mxfp4 instead.  Nothing but the routing's sort runs between the
 kernels, no step waits for the host, and the sizes the kernels need to know
 (how many rows each expert got) stay on the GPU.
 
+The router reads the normalised rows as the int8 codes give them, so where two
+experts' logits lie close together it may choose the other one.
+
 Run as a program it checks the layer against a plain float64 evaluation of the
-same weights, prints the error, and times it.
+same weights with the same routing, prints the error and how many choices a
+float64 router would have made differently, and times it.
 """
 import argparse
 import os
@@ -93,14 +97,32 @@ class MoELayer:
         out = (y[place] * weight[..., None]).sum(1)
         return out.to(t), h
 
-    def plain(self, x, residual):
-        """The layer in float64 on the stored (quantised) weights, without
-        rounding any activation; routed as the layer routes."""
+    def chosen(self, n):
+        """The experts that the router takes for each row of n: T x top."""
+        return torch.softmax(n @ self.router.t().to(n.dtype), dim=1).topk(self.top, dim=1).indices
+
+    def normalised(self, x, residual):
+        """(h, the normalised rows in float64, those the layer's router reads,
+        which are rounded to int8 codes)."""
         h = (x.double() + residual.double()).to(x.dtype)
         d = h.double()
         n = d / torch.sqrt((d * d).mean(1, keepdim=True) + self.eps) * self.norm.double()
         q, scale, _ = lp.add_rmsnorm_quantize(x, self.norm, self.eps, residual=residual)
-        _, chosen = torch.softmax((q * scale[:, None]).to(x.dtype) @ self.router.t().to(x.dtype), dim=1).topk(self.top, dim=1)
+        return h, n, (q * scale[:, None]).to(x.dtype)
+
+    def routing_changes(self, x, residual):
+        """The share of the T x top choices that float64 would not have made:
+        rounding the rows moves experts whose logits lie close together."""
+        _, n, rounded = self.normalised(x, residual)
+        exact = torch.zeros(len(n), self.G, dtype=torch.bool, device=n.device).scatter_(1, self.chosen(n), True)
+        return 1 - exact.gather(1, self.chosen(rounded)).double().mean().item()
+
+    def plain(self, x, residual):
+        """The layer in float64 on the stored (quantised) weights, without
+        rounding any activation; routed as the layer routes, so what rounding
+        changes in the routing (`routing_changes`) is not in the difference."""
+        h, n, rounded = self.normalised(x, residual)
+        chosen = self.chosen(rounded)
         p = torch.gather(torch.softmax(n @ self.router.double().t(), dim=1), 1, chosen)
         p = p / p.sum(1, keepdim=True)
         out = torch.zeros_like(n)
@@ -144,6 +166,7 @@ def main():
         out, _ = layer(x, r)
         ref, _ = layer.plain(x, r)
         err = ((out.double() - ref).norm() / ref.norm()).item()
+        moved = layer.routing_changes(x, r)
         for _ in range(5):
             layer(x, r)
         torch.cuda.synchronize()
@@ -152,7 +175,8 @@ def main():
             layer(x, r)
         torch.cuda.synchronize()
         print(f"{args.format} {T} tokens: {(time.perf_counter() - t0) / 20 * 1e6:.0f} us, "
-              f"error against float64 {err:.2e}", flush=True)
+              f"error against float64 {err:.2e} with the same routing, "
+              f"{100 * moved:.1f}% of the choices differ from float64's", flush=True)
 
 
 if __name__ == "__main__":

@@ -40,3 +40,32 @@ def test_layer(fmt, bound, T, dtype):
     ref, href = layer.plain(x, r)
     assert out.dtype == dtype and torch.equal(h, href)
     assert ((out.double() - ref).norm() / ref.norm()).item() < bound
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_routing_changes(dtype):
+    """None where the experts' logits lie far apart; two of three where the
+    choices share one; else what a plain loop over float64 logits counts."""
+    layer = moe_layer.random_layer(12, 512, 32, 3, "w8a8", dtype, seed=1)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    r = torch.zeros(200, 512, device="cuda", dtype=dtype)
+    # token t is made of the rows of experts t, t + 1 and t + 2, in falling parts
+    e = torch.eye(12, device="cuda").double()
+    part = 4 * e + 3 * e.roll(1, 1) + 2 * e.roll(2, 1)
+    layer.norm = torch.ones_like(layer.norm)
+    layer.router = torch.nn.functional.one_hot(torch.arange(12, device="cuda"), 512).to(dtype)
+    x = torch.zeros(12, 512, device="cuda", dtype=dtype)
+    x[:, :12] = part.to(dtype)
+    assert layer.routing_changes(x, r[:12]) == 0
+    layer.router = torch.randn(12, 512, generator=g, device="cuda").to(dtype) / 20
+    x = torch.randn(200, 512, generator=g, device="cuda").to(dtype)
+    _, n, rounded = layer.normalised(x, r)
+    logits = n @ layer.router.double().t()
+    kept = 0
+    for t in range(200):
+        best = set(sorted(range(12), key=lambda i: -logits[t, i].item())[:3])
+        kept += len(best & set(layer.chosen(rounded)[t].tolist()))
+    assert layer.routing_changes(x, r) == pytest.approx(1 - kept / 600, abs=1e-12)
+    layer.chosen = lambda rows: torch.full((200, 3), 5, device="cuda") + torch.arange(3, device="cuda") * (
+        1 if rows.dtype == torch.float64 else -1)
+    assert layer.routing_changes(x, r) == pytest.approx(2 / 3)      # 5, 6, 7 and 5, 4, 3 share one
