@@ -65,13 +65,19 @@ inline GroupedCfg choose_grouped(int kind, int64_t rows, int64_t groups, int64_t
   auto fills = [&](GroupedCfg c, int64_t percent) { return 100 * grid(c) >= percent * cu_count; };
   // percent of a round of `slots` workgroups; the first four rounds count whole
   auto rounds = [](int64_t t, int64_t slots) { return t <= 4 * slots ? 100 * ((t + slots - 1) / slots) : 100 * t / slots; };
-  // MXFP4 experts whose weights are more than the 256 MiB Infinity Cache keeps
-  // from one call to the next, and mostly read by one row tile: B streams
-  // non-temporally (64 experts of 2048 x 4096, 10 rows each 52.9 against 58.6
-  // us; 128 of 4096 x 4096, 4 rows each 191 against 207; with weights of 67 MB
-  // that stay cached 1.3-1.4 times slower, with rows that do not start on a
-  // cache line 1.25 times: each line is fetched twice; at K = 1024, four
-  // lines a row, no faster: 64 of 7168 x 1024 26.6 against 25.6)
+  // MXFP4 experts with 100 MiB of weights and more, mostly read by one row
+  // tile: B streams non-temporally.  A model's layers together hold more than
+  // the 256 MiB Infinity Cache, so the weights are taken not to be in it when
+  // the call comes.  Then the stream is faster at every size (us with and
+  // without, 8 rows an expert: 64 experts of 2048 x 2048, 128 MiB, 29.5, 32.6;
+  // 32 of 7168 x 2048, 224 MiB, 50.3, 53.7; 64 of 2048 x 4096, 256 MiB, 50.1,
+  // 57.0; 128 of 4096 x 4096, 1 GiB, 193, 212).  A call that repeats on the
+  // same weights pays below 256 MiB, as it finds less of them cached (29.0,
+  // 26.5; 49.7, 43.7), and gains from there on (50.4, 51.6; 198, 219).  Below
+  // 100 MiB the weights of two such calls fit in the cache together: plain
+  // loads.  Rows that do not start on a cache line: 1.25 times slower, each
+  // line is fetched twice.  K = 1024, four lines a row: no faster (64 of 7168 x
+  // 1024 26.6 against 25.6).
   // (divided by the groups: the product of all three may pass 64 bits)
   const int64_t least = (((int64_t)100 << 20) + groups - 1) / groups;
   if (mxfp4 && !one && row_bytes % 128 == 0 && row_bytes > 512 && N * row_bytes >= least) {
