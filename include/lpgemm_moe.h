@@ -124,7 +124,8 @@ lpgemm_status lpgemm_mxfp4(int64_t M, int64_t N, int64_t K, const uint8_t *A, co
  * group are left as they were; where groups overlap, what C holds is
  * undefined.  A row_index outside 0..a_rows-1 gives a row of zeros.
  * With a row_index the tokens A must stay below 2 GiB (UNSUPPORTED_SHAPE).
- * groups = 0, rows = 0 or N = 0 is a no-op; K = 0 sets the grouped rows to 0;
+ * groups = 0, rows = 0 or N = 0 is a no-op; K = 0 leaves empty sums, grouped
+ * rows of 0 (int8: 0 times the scales);
  * a_rows = 0 with rows > 0 needs a row_index and gives rows of zeros.
  * groups is at most LPGEMM_MAX_GROUPS, rows and N at most 2^31 - 257, and the
  * tiles of C must fit one launch (below 2^24 workgroups; UNSUPPORTED_SHAPE

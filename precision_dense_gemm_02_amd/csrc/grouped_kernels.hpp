@@ -240,10 +240,13 @@ __device__ __forceinline__ void store1(const GroupedArgs& p, size_t idx, float v
 // BNT: B streams non-temporally, where it is read once.
 //
 // Bound by operand latency and power where a tile has many rows (256 x 256:
-// MXFP4 8192^3 250 us, 4.4 PFLOP/s, without its operand loads 210; int8, 8
-// experts of 1024 rows, 14336 x 4096, 521 us, 1.85 POP/s), by the weights
-// where it has few (MXFP4, 64 experts of 32 rows, 2048 x 4096, 53.4 us, 5.3
-// TB/s).
+// MXFP4 8192^3 259 us, 4.2 PFLOP/s, without its operand loads 210; int8, 8
+// experts of 1024 rows, 14336 x 4096, 524 to 541 us on several cards, 1.8
+// POP/s), by the weights where it has few (MXFP4, 64 experts of 32 rows, 2048 x
+// 4096, 54 to 63 us, 4.7 to 5.5 TB/s), and in between, where a CU gets one or
+// two tiles of 100 rows and more, by the latency of each stage, which two
+// stages do not hide (int8, 4 experts of 242 rows each, 4096 x 4096, 37.5 us,
+// of 120 to 300 rows 44.9, 1.2 and 1.4 a stage; the floor is 15.6).
 template <int KIND, int BM, int BN, int WM, int WN, int STAGES, bool PIN, bool TAIL, bool BNT = false>
 __global__ __launch_bounds__(256) void grouped_tile(GroupedArgs p) {
   using Acc = typename GroupedAcc<KIND>::type;
@@ -321,7 +324,8 @@ __global__ __launch_bounds__(256) void grouped_tile(GroupedArgs p) {
   }
   // scale slot t of this wave: rows 32 (4 t + wave) + lane / 2, 16 of their 32
   // bytes; the halves of every second 8 rows change places, so that the words
-  // of 16 consecutive rows lie in different banks
+  // of 16 consecutive rows lie in different banks (those of rows 16 apart do
+  // not)
   const int sc_half = ((lane & 1) ^ ((lane >> 4) & 1)) * 16;
   uint32_t sc_off[MX ? kSc : 1];
   if constexpr (MX) {
@@ -619,7 +623,7 @@ __global__ __launch_bounds__(256) void grouped_tile(GroupedArgs p) {
 //
 // Bound by the weights' stream from HBM; the ring keeps WAVES x (DEPTH - 1) x
 // 4 KiB of it in flight per workgroup (int8, 8 of 64 experts of 2048 x 4096 on
-// one token 12.2 us, 5.5 TB/s; MXFP4, 16 rows of 14336 x 4096 8.5 us, 3.8).
+// one token 12.2 us, 5.5 TB/s; MXFP4, 16 rows of 14336 x 4096 8.8 us, 3.7).
 template <int KIND, int WAVES, int DEPTH, int AG>
 __global__ __launch_bounds__(WAVES * 64) void grouped_skinny(GroupedArgs p) {
   using Acc = typename GroupedAcc<KIND>::type;

@@ -233,9 +233,9 @@ __device__ __forceinline__ float lifted_squares(const i32x4& h, float sumsq) {
 // otherwise.
 //
 // Bound by HBM from a few hundred rows on (norm 7, activation 5 bytes a value;
-// bfloat16, inputs in no cache: norm of 8192 x 8192 83.5 us, 5.6 TB/s; the
-// activation of 4096 x 14336 55.1, 5.3 TB/s), below that by the launch and a
-// trip to memory (1 x 4096 2.7 us, 16 x 14336 4.1).  Non-temporal stores would
+// bfloat16, inputs in no cache: norm of 8192 x 8192 80.7 us, 5.8 TB/s; the
+// activation of 4096 x 14336 50.9, 5.8 TB/s), below that by the launch and a
+// trip to memory (1 x 4096 2.7 us, 16 x 14336 4.4).  Non-temporal stores would
 // take 2 to 5% off the large ones and slow the product that reads the codes
 // by more (activation of 4096 x 14336 and the product with 4096 columns 249
 // against 234 us; 1024 rows 116 against 118).
@@ -317,8 +317,8 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) void rows_int8_regs(RowA
 }
 
 // Longer rows (and K = 0): a workgroup per row and two passes over it, the
-// second mostly from the L2 (norm of 4096 x 40000 249 us, 4.6 TB/s; activation
-// of 2048 x 40000 114, 3.6 TB/s).  A thread handles the same chunks in all, so
+// second mostly from the L2 (us, norm of 2048 x 40000 131, 4.4 TB/s; activation
+// of 2048 x 40000 112, 3.7 TB/s, its exponentials twice).  A thread handles the same chunks in all, so
 // a later one may read back an H that overwrote X or R.
 template <typename T, bool NORM>
 __global__ __launch_bounds__(1024) void rows_int8_long(RowArgs p) {

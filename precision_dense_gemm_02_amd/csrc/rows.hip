@@ -24,8 +24,8 @@ lpgemm_status enqueue(const void* fn, int64_t grid, int threads, void* args, hip
 // (bfloat16, us on one MI355X with 1, 2, 4, 8 and 16 wavefronts; norm, 8192
 // rows of 512: 9.7 10.8 14.8 23.5 45.3; of 1024: 15.1 15.6 18.5 27.0 49.8; of
 // 4096: 50.2 46.8 44.5 46.1 60.4; of 8192: - 89.2 86.0 84.6 90.3; of 14336: -
-// - 148 146 146; activation, 8192 rows of 14336: - - 113 113 106; 16 rows: - -
-// 4.7 4.0 4.0; 8192 rows of 32768: - - - 243 238, and 349 in two passes).
+// - 148 146 146; activation, 8192 rows of 14336: - - 112 113 106; 16 rows: - -
+// 5.1 4.4 4.4; 8192 rows of 32768: - - - 245 236, and 337 in two passes).
 template <typename T, bool NORM>
 lpgemm_status launch_rows(RowArgs& p, hipStream_t stream) {
   const int K = p.K;
