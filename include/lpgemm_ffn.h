@@ -1,0 +1,150 @@
+/*
+ * lpgemm: 4-bit weights with group scales, and the gated feed-forward block,
+ * for one AMD Instinct MI355X (gfx950).
+ *
+ *   lpgemm_quantize_w4, lpgemm_dequantize_w4   16-bit weights to 4-bit codes,
+ *                             one scale (and zero point) per group along k
+ *   lpgemm_w4                 C = X . W^T for 16-bit rows and such weights
+ *   lpgemm_gated_w4           act(X . G^T) * (X . U^T) for such weights
+ *   lpgemm_gated_ffn          (act(X . G^T) * (X . U^T)) . D^T, 16-bit weights
+ *   lpgemm_gated_ffn_backward its gradients
+ *
+ * The conventions of lpgemm.h and lpgemm_moe.h hold: device pointers owned by
+ * the caller, work enqueued on `stream` without synchronising, nothing
+ * allocated, no state kept between calls, the same status codes checked on the
+ * host in the same order (sizes, shape rules, empty problem, NULL pointers,
+ * alignment, workspace, then the device and the launch).  Weights are N rows
+ * of K values.  Outputs must not overlap inputs, each other or the workspace.
+ *
+ * Sixteen-bit tensors are binary16 or bfloat16; `type` is the type of every
+ * 16-bit tensor of a call.  Sums are held in binary32; their order depends on
+ * the sizes only, so equal calls give equal bits.  Infinities and NaN go the
+ * way the formulas send them.
+ *
+ * Workspaces are scratch: a call writes every byte that it reads, nothing has
+ * to be cleared, and nothing is kept from one call for the next.  Calls that
+ * share one must not overlap in time.
+ */
+#ifndef LPGEMM_FFN_H
+#define LPGEMM_FFN_H
+
+#include "lpgemm_moe.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* The activation of a gated block:
+ *   LPGEMM_SILU  g / (1 + exp(-g))
+ *   LPGEMM_GELU  g (1 + tanh(z)) / 2 = g / (1 + exp(-2 z)),
+ *                z = sqrt(2 / pi) (g + 0.044715 g^3) */
+typedef enum lpgemm_activation {
+    LPGEMM_SILU = 0,
+    LPGEMM_GELU = 1
+} lpgemm_activation;
+
+/* Weights in 4 bits.  W is N x K; `group` consecutive values of a row share a
+ * scale and, where there are zero points, a zero:
+ *   W[n][k] = (code[n][k] - zero[n][k / group]) * scale[n][k / group].
+ * Codes are signed (-8..7), two to a byte along k, the even k in the low
+ * nibble, two's complement: N rows of K / 2 bytes, the operand layout of
+ * lpgemm_i4.  Scales and zeros are N x (K / group) values of a 16-bit type;
+ * zeros may hold any value, integers or not, and NULL stands for zeros of 0.
+ * group is 32, 64, 128 or 256 and divides K; K is at most LPGEMM_MAX_K_W4. */
+#define LPGEMM_MAX_K_W4 1048576
+
+/* W of `type` to codes, scales and (zeros not NULL) zeros.  For each group,
+ * in binary32 and rounded to nearest even:
+ *   without zeros: s = type(max |w| / 7), code = clamp(rne(w / s), -8, 7);
+ *   with zeros: lo = min(0, min w), hi = max(0, max w), s = type((hi - lo) / 15),
+ *     zero = clamp(-8 - rne(lo / s), -8, 7), an integer,
+ *     code = clamp(rne(w / s) + zero, -8, 7).
+ * A group whose max |w| (hi - lo) is below 2^-100, or whose s is 0, gets s = 0
+ * and codes and zero 0; one with an infinity or a NaN gets s = NaN and codes
+ * and zero 0; where hi - lo leaves binary32 (bfloat16 near its largest), s is
+ * an infinity, codes and zero 0.
+ * w_stride in elements, at least K, a multiple of 8.  Pointers 16-byte
+ * aligned, scales and zeros 2-byte.  N = 0 or K = 0 is a no-op. */
+lpgemm_status lpgemm_quantize_w4(int64_t N, int64_t K, int64_t group, lpgemm_type type, const void *W,
+                                 int64_t w_stride, uint8_t *codes, void *scales, void *zeros,
+                                 hipStream_t stream);
+
+/* The values the codes stand for: Y = N x K of `out_type` (any of the three),
+ * (code - zero) * scale, each operation rounded to binary32, then once to
+ * out_type.  `type`: that of scales and zeros. */
+lpgemm_status lpgemm_dequantize_w4(int64_t N, int64_t K, int64_t group, lpgemm_type type, const uint8_t *codes,
+                                   const void *scales, const void *zeros, lpgemm_type out_type, void *Y,
+                                   hipStream_t stream);
+
+/* C = X . W^T: X M rows of K values of `type` (x_stride in elements, at least
+ * K, a multiple of 8, at most LPGEMM_MAX_STRIDE), W in 4 bits with scales and
+ * zeros of the same type, C M x N of `out_type`.  The weights enter the sums
+ * exactly: C[m][n] = sum over groups of scale * (sum of x * code - zero * sum
+ * of x), every sum in binary32.  A row of X with an infinity or a NaN gives NaN
+ * (the kernels sum x * (code + 24) and take 24 times the sum of x off), and so
+ * may one with magnitudes above 2^115.  M = 0 or N = 0 is a no-op; K = 0 sets C
+ * to 0.
+ * X, codes and C 16-byte aligned, scales and zeros 2-byte.  M and N at most
+ * 2^31 - 257 and below 2^24 tiles of C (UNSUPPORTED_SHAPE otherwise).
+ * `workspace`, 16-byte aligned, holds at least lpgemm_w4_workspace(M, K, group)
+ * bytes (0 up to LPGEMM_W4_SHORT_M rows; -1 for sizes out of range);
+ * INVALID_VALUE where it is missing or too small. */
+#define LPGEMM_MAX_STRIDE 2097152
+#define LPGEMM_W4_SHORT_M 64
+int64_t lpgemm_w4_workspace(int64_t M, int64_t K, int64_t group);
+lpgemm_status lpgemm_w4(int64_t M, int64_t N, int64_t K, int64_t group, lpgemm_type type, const void *X,
+                        int64_t x_stride, const uint8_t *codes, const void *scales, const void *zeros,
+                        lpgemm_type out_type, void *C, void *workspace, int64_t workspace_bytes,
+                        hipStream_t stream);
+
+/* H = act(X . G^T) * (X . U^T), M x F of out_type, where the first F of the 2 F
+ * weight rows are G and the others U; both products, the activation and the
+ * product of the two in binary32, rounded once.  Otherwise as lpgemm_w4 with
+ * N = 2 F. */
+lpgemm_status lpgemm_gated_w4(int64_t M, int64_t F, int64_t K, int64_t group, lpgemm_type type,
+                              lpgemm_activation activation, const void *X, int64_t x_stride,
+                              const uint8_t *codes, const void *scales, const void *zeros, lpgemm_type out_type,
+                              void *H, void *workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/* The gated feed-forward block with 16-bit weights, everything of `type`:
+ *   [g u] = X . W_gate_up^T    X: M x D, W_gate_up: 2 F x D, gate rows first
+ *   h = act(g) * u             from the binary32 sums, rounded to `type`
+ *   Y = h . W_down^T           W_down: D x F, Y: M x D
+ * GU, if not NULL, receives [g u] (M x 2 F, each rounded once), which the
+ * backward pass reads.  D and F are multiples of 8, at most LPGEMM_MAX_D_FFN;
+ * M at most 2^31 - 257, with below 2^24 tiles of 64 x 64 of each M x 2 F, M x D
+ * and 2 F x D matrix.  x_stride as for lpgemm_w4.  Pointers 16-byte aligned.
+ * M = 0 is a no-op; F = 0 sets Y to 0, D = 0 sets GU to 0.
+ * `workspace`, 256-byte aligned, holds at least
+ * lpgemm_gated_ffn_workspace(M, D, F) bytes, which depends on the current
+ * device's number of compute units (-1 for sizes out of range or no device). */
+#define LPGEMM_MAX_D_FFN 262144
+int64_t lpgemm_gated_ffn_workspace(int64_t M, int64_t D, int64_t F);
+lpgemm_status lpgemm_gated_ffn(int64_t M, int64_t D, int64_t F, lpgemm_type type, lpgemm_activation activation,
+                               const void *X, int64_t x_stride, const void *W_gate_up, const void *W_down,
+                               void *GU, void *Y, void *workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/* The block's gradients, from dY (M x D, dy_stride as x_stride) and what the
+ * forward pass had and kept:
+ *   dh = dY . W_down, h = act(g) * u, du = dh act(g), dg = dh u act'(g)
+ *   dX = [dg du] . W_gate_up            M x D, of `type`
+ *   dW_gate_up = [dg du]^T . X          2 F x D, of grad_type
+ *   dW_down = dY^T . h                  D x F, of grad_type
+ * h, dg and du are formed in binary32 from GU and the binary32 sums dh and
+ * rounded once to `type`, as operands of the products behind them.  grad_type
+ * is LPGEMM_F32 or `type`.  Any of dX, dW_gate_up and dW_down may be NULL: it
+ * is then not computed.  M = 0 sets the weights' gradients to 0, F = 0 sets dX
+ * to 0; D = 0 is a no-op. */
+int64_t lpgemm_gated_ffn_backward_workspace(int64_t M, int64_t D, int64_t F);
+lpgemm_status lpgemm_gated_ffn_backward(int64_t M, int64_t D, int64_t F, lpgemm_type type,
+                                        lpgemm_activation activation, const void *dY, int64_t dy_stride,
+                                        const void *X, int64_t x_stride, const void *W_gate_up,
+                                        const void *W_down, const void *GU, lpgemm_type grad_type, void *dX,
+                                        void *dW_gate_up, void *dW_down, void *workspace,
+                                        int64_t workspace_bytes, hipStream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* LPGEMM_FFN_H */

@@ -13,6 +13,8 @@ and the seeded input generators (inputs.py).
 The operators of a quantised expert layer (include/lpgemm_moe.h, bound in
 _moe.py) stand beside the GEMMs: residual + RMSNorm and silu(gate) * up with
 int8 rows, MXFP4 quantisation and product, and products grouped by expert.
+So do 4-bit weights with group scales and the gated feed-forward block with
+its gradients (include/lpgemm_ffn.h, bound in _ffn.py).
 """
 from ._binding import (LpgemmError, auto_config, config_count, f64_emu_moduli, force_config, f64_emu_workspace_bytes, gemm_f16, gemm_f64_emu, gemm_f64_emu_noalloc, gemm_i4, gemm_i4_e3m2, gemm_i4_via_e3m2,  # noqa: F401
                        gemm_f16_splitk, gemm_i4_splitk, gemm_i8_dequant_splitk, gemm_i8_splitk,
@@ -31,13 +33,21 @@ __all__ = ["LpgemmError", "gemm_i8", "gemm_i8_kxn", "gemm_i4", "gemm_f16", "gemm
 _MOE = ("add_rmsnorm_quantize", "silu_mul_quantize", "quantize_mxfp4", "dequantize_mxfp4", "mxfp4_scale_stride",
         "gemm_mxfp4", "gemm_i8_dequant_grouped", "gemm_f16_grouped", "gemm_mxfp4_grouped", "grouped_config_count",
         "force_grouped_config", "grouped_auto_config")
-__all__ += _MOE
+# ... and those of 4-bit weights and of the gated feed-forward block
+_FFN = ("quantize_w4", "dequantize_w4", "gemm_w4", "gated_gemm_w4", "gated_ffn", "gated_ffn_backward",
+        "gated_ffn_workspace_bytes", "gated_ffn_backward_workspace_bytes")
+__all__ += _MOE + _FFN
 
 
 def __getattr__(name):
-    if name not in _MOE:
+    if name in _MOE:
+        from . import _moe as module
+        names = _MOE
+    elif name in _FFN:
+        from . import _ffn as module
+        names = _FFN
+    else:
         raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
-    from . import _moe
-    for n in _MOE:
-        globals()[n] = getattr(_moe, n)
+    for n in names:
+        globals()[n] = getattr(module, n)
     return globals()[name]

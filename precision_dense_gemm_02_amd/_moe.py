@@ -33,13 +33,14 @@ _SIGNATURES = {
     "lpgemm_mxfp4_grouped": [_i64, _i64, _i64, _i64, _i64, _p, _p, _p, _p, _p, _p, _int, _p, _p],
 }
 _functions: dict = {}
+_SIGNATURES_ELSEWHERE: dict = {}   # of entry points bound in other modules
 
 
 def _function(name: str):
     f = _functions.get(name)
     if f is None:
         f = getattr(load_library(), name)
-        f.argtypes = _SIGNATURES[name]
+        f.argtypes = _SIGNATURES.get(name) or _SIGNATURES_ELSEWHERE[name]
         f.restype = ctypes.c_int
         _functions[name] = f
     return f

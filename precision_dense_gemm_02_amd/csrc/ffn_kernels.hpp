@@ -1,0 +1,400 @@
+// The products of the gated feed-forward block and of its gradients, on 16-bit
+// operands:
+//
+//   C = A . B   M x N over K,   A(m, k), B(k, n)
+//
+// Either operand may lie along k (rows of K values, as activations and
+// weights do in the forward pass) or across it (K rows of M or N values: the
+// gradients read the same arrays the other way).
+#pragma once
+
+#include "activation.hpp"
+#include "half_types.hpp"
+
+namespace lpgemm {
+
+// What becomes of a tile of sums.
+enum TileEnd {
+  END_STORE = 0,       // C, in out_type
+  END_GATED = 1,       // columns are pairs gate, up: H = act(gate) * up, and [gate up] if GU is set
+  END_GATED_GRAD = 2,  // sums are dh: from [gate up] in GU, [dg du] into DGU and h into H
+};
+
+struct TileArgs {
+  const uint8_t* A;
+  const uint8_t* B;        // END_GATED: the gate's rows, then F rows of the up projection
+  int64_t a_stride;        // bytes from one stored row to the next
+  int64_t b_stride;
+  uint8_t* C;              // END_STORE: rows of N values
+  int out_type;            // ... lpgemm_type
+  uint8_t* H;              // M x F
+  uint8_t* GU;             // M x 2 F
+  uint8_t* DGU;            // M x 2 F
+  int activation;
+  int M, N, K;             // END_GATED: N = 2 F, END_GATED_GRAD: N = F
+  int F;
+  int k_stages;            // K-stages of 64, all of them
+  int split_stages;        // ... of one split (blockIdx.y)
+  int splits;
+  float* part;             // splits > 1: splits x M x N sums
+  int tiles_m, tiles_n;
+};
+
+// Chunk position of 16-byte chunk `c` in a stage row k of an operand that lies
+// across k (COLS values a row): pairs of chunks move by an even number that
+// differs between the four k-rows one transposing read takes, so that they
+// fall on different banks.
+template <int COLS>
+__device__ __forceinline__ int across_shift(int k) {
+  return COLS >= 128 ? 2 * (k & 3) : 2 * ((k >> 1) & 1);
+}
+
+// Eight consecutive columns of one row: what END does with them.  `v`: the sums
+// (END_GATED: of the gate), `u`: those of the up projection.
+template <typename T, int END>
+__device__ __forceinline__ void finish8(const TileArgs& p, int row, int col, const float (&v)[8], const float (&u)[8]) {
+  if constexpr (END == END_STORE) {
+    const size_t at = (size_t)row * p.N + col;
+    if (p.out_type == 0) {
+      f32x4* c = (f32x4*)(p.C + 4 * at);
+      c[0] = f32x4{v[0], v[1], v[2], v[3]};
+      c[1] = f32x4{v[4], v[5], v[6], v[7]};
+    } else {
+      *(i32x4*)(p.C + 2 * at) = narrow8<T>(v);
+    }
+  } else if constexpr (END == END_GATED) {
+    float h[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[e] = activate(v[e], p.activation) * u[e];
+    if (p.GU) {
+      uint8_t* gu = p.GU + 2 * ((size_t)row * 2 * p.F + col);
+      *(i32x4*)gu = narrow8<T>(v);
+      *(i32x4*)(gu + 2 * (size_t)p.F) = narrow8<T>(u);
+    }
+    *(i32x4*)(p.H + 2 * ((size_t)row * p.F + col)) = narrow8<T>(h);
+  } else {
+    const size_t at = 2 * ((size_t)row * 2 * p.F + col);
+    const f32x8 g = widen<T>(*(const i32x4*)(p.GU + at)), up = widen<T>(*(const i32x4*)(p.GU + at + 2 * (size_t)p.F));
+    float dg[8], du[8], h[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      float act, slope;
+      activate_with_slope(g[e], p.activation, act, slope);
+      dg[e] = v[e] * up[e] * slope;
+      du[e] = v[e] * act;
+      h[e] = act * up[e];
+    }
+    *(i32x4*)(p.DGU + at) = narrow8<T>(dg);
+    *(i32x4*)(p.DGU + at + 2 * (size_t)p.F) = narrow8<T>(du);
+    *(i32x4*)(p.H + 2 * ((size_t)row * p.F + col)) = narrow8<T>(h);
+  }
+}
+
+// The splits' sums added in order, eight columns per lane.
+template <typename T, int END>
+__global__ __launch_bounds__(256) void join_splits(TileArgs p) {
+  const int columns = END == END_GATED ? p.F : p.N;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int chunks = columns / 8;
+  const int row = (int)(i / chunks), col = 8 * (int)(i - (int64_t)row * chunks);
+  if (row >= p.M) return;
+  float v[8] = {}, u[8] = {};
+  for (int s = 0; s < p.splits; ++s) {
+    const float* part = p.part + ((size_t)s * p.M + row) * p.N + col;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const f32x4 a = *(const f32x4*)(part + 4 * q);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[4 * q + e] += a[e];
+      if constexpr (END == END_GATED) {
+        const f32x4 b = *(const f32x4*)(part + p.F + 4 * q);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) u[4 * q + e] += b[e];
+      }
+    }
+  }
+  finish8<T, END>(p, row, col, v, u);
+}
+
+// BM x BN tiles, four waves in a WM x WN grid, a ring of STAGES K-stages of 64.
+// A stage holds an operand's rows of 128 bytes along k, or its 64 k-rows
+// across it; both arrive by 16-byte direct-to-LDS loads, swizzled, and leave
+// as 32 x 16 fragments: one ds_read_b128, or two transposing ds_read_b64.  Lane
+// l has k = 32 (l / 32) + 8 kk .. + 7 of the stage in K-step kk for both.
+//
+// The loads of stage s + STAGES - 1 go out in the first two K-steps of stage s,
+// one matrix instruction pinned in front of each; one barrier per stage, in its
+// last K-step, publishes stage s + 1, whose first fragments are read while the
+// rest of stage s's products run.
+//
+// END_GATED: a wave's columns are WTN / 2 of the gate and the same of the up
+// projection, so that both sums of an element meet in one lane.
+template <typename T, bool A_ACROSS, bool B_ACROSS, int BM, int BN, int WM, int WN, int STAGES, int END>
+__global__ __launch_bounds__(256) void ffn_tile(TileArgs p) {
+  using Layout = RowLayout<128>;
+  constexpr int WTM = BM / WM, WTN = BN / WN;
+  constexpr int TM = WTM / 32, TN = WTN / 32;
+  static_assert(WM * WN == 4 && TM >= 1 && TN >= 1 && WTM % 32 == 0 && WTN % 32 == 0, "wave tiles");
+  static_assert(END != END_GATED || (!B_ACROSS && TN % 2 == 0), "gate and up columns in one wave");
+  constexpr bool GATED = END == END_GATED;
+  constexpr int kRows = BM + BN, kStage = kRows * 128;
+  constexpr int kSlots = kRows / 32, kSlotsA = BM / 32;   // 1 KiB loads per wave and stage
+  constexpr int kEpiPitch = WTN * 4 + 32;
+  constexpr int kEpiRows = WTM < 64 ? WTM : 64;
+  constexpr int kEpiWave = kEpiRows * kEpiPitch;
+  constexpr int kLds = STAGES * kStage > 4 * kEpiWave ? STAGES * kStage : 4 * kEpiWave;
+  static_assert(kLds <= 160 * 1024, "LDS");
+  constexpr int kInFlight = (STAGES - 2) * kSlots;
+  static_assert(STAGES >= 2 && kInFlight + kSlots <= 63, "vmcnt range");
+
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[kLds];
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+
+  // bands of 8 row tiles, column tile by column tile; every XCD a contiguous range
+  const int logical = xcd_logical(blockIdx.x, p.tiles_m * p.tiles_n);
+  const int band = logical / (8 * p.tiles_n), in_band = logical - band * 8 * p.tiles_n;
+  const int height = min(p.tiles_m - 8 * band, 8);
+  const int m0 = (8 * band + in_band % height) * BM;
+  constexpr int kTileColumns = GATED ? BN / 2 : BN;
+  const int n0 = (in_band / height) * kTileColumns;
+  const int columns = GATED ? p.F : p.N;
+  const int rows = min(BM, p.M - m0), cols = min(kTileColumns, columns - n0);
+
+  const int s_begin = blockIdx.y * p.split_stages;
+  const int s_end = min(s_begin + p.split_stages, p.k_stages);
+
+  const uint8_t* const a_base = A_ACROSS ? p.A + 2 * (size_t)m0 : p.A + (size_t)m0 * p.a_stride;
+  const uint8_t* const b_base = B_ACROSS ? p.B + 2 * (size_t)n0 : p.B + (size_t)n0 * p.b_stride;
+  const uint32_t smem_lds = lds_address(smem);
+
+  // Load slot t of this wave fills 1 KiB of a stage.  Along k: stage rows 32 t +
+  // 8 wave .. + 7, eight lanes a row.  Across: 1024 / (2 BX) k-rows.  A lane
+  // fetches the chunk whose swizzled place is its own.
+  const int lrow = 8 * wave + lane / 8;
+  const uint32_t along_col = Layout::pos(lrow, lane % 8) * 16;   // (rows 32 apart have the same swizzle)
+  uint32_t off[kSlots];
+#pragma unroll
+  for (int t = 0; t < kSlots; ++t) {
+    const bool is_a = t < kSlotsA;
+    const int u = is_a ? t : t - kSlotsA;
+    if (is_a ? A_ACROSS : B_ACROSS) {
+      const int bx = is_a ? BM : BN, per_row = bx / 8;
+      const int k = (4 * u + wave) * (64 / per_row) + lane / per_row, at = lane % per_row;
+      const int shift = is_a ? across_shift<BM>(k) : across_shift<BN>(k);
+      const int c = (((at >> 1) ^ shift) << 1) | (at & 1);
+      off[t] = 8 * c < (is_a ? rows : cols) ? (uint32_t)(k * (is_a ? p.a_stride : p.b_stride)) + 16 * c : kOutOfRange;
+    } else if (is_a || !GATED) {
+      off[t] = (uint32_t)((32 * u + lrow) * (is_a ? p.a_stride : p.b_stride)) + along_col;
+    } else {   // 32-row block u of B: gate or up columns of wave column 32 u / WTN
+      const int c = 32 * u / WTN * (WTN / 2) + 32 * u % (WTN / 2) + lrow;
+      off[t] = (uint32_t)(c * p.b_stride) + along_col;
+    }
+  }
+  const bool has_up = GATED;
+  const uint32_t row_bytes = 2 * (uint32_t)p.K;
+  const i32x4 rsrc_a_along = make_rsrc(a_base, A_ACROSS ? 0 : (uint32_t)(rows * p.a_stride));
+  const i32x4 rsrc_b_along = make_rsrc(b_base, B_ACROSS ? 0 : (uint32_t)(cols * p.b_stride));
+  const i32x4 rsrc_up = make_rsrc(has_up ? b_base + (size_t)p.F * p.b_stride : b_base, has_up ? (uint32_t)(cols * p.b_stride) : 0);
+  // across k, a stage's k-rows have a descriptor of their own: the whole operand may be larger than 4 GiB
+  auto across_rsrc = [&](const uint8_t* base, int64_t stride, int s) {
+    const int left = s < s_end ? min(p.K - 64 * s, 64) : 0;
+    return make_rsrc(base + (int64_t)64 * s * stride, (uint32_t)(left * stride));
+  };
+  i32x4 rsrc_a = rsrc_a_along, rsrc_b = rsrc_b_along;
+  auto enter_stage = [&](int s) {   // the descriptors for the loads of stage s
+    if constexpr (A_ACROSS) rsrc_a = across_rsrc(a_base, p.a_stride, s);
+    if constexpr (B_ACROSS) rsrc_b = across_rsrc(b_base, p.b_stride, s);
+  };
+  auto issue_load = [&](int t, int s, int slot) __attribute__((always_inline)) {
+    const bool is_a = t < kSlotsA;
+    const uint32_t to = smem_lds + slot * kStage + (4 * t + wave) * 1024;
+    uint32_t from = off[t];
+    if (!(is_a ? A_ACROSS : B_ACROSS)) {
+      const uint32_t kbyte = (uint32_t)s * 128;
+      from = s < s_end && kbyte + along_col < row_bytes ? from + kbyte : kOutOfRange;
+    }
+    if (is_a) lds_dma_16(rsrc_a, to, from);
+    else if (GATED && (32 * (t - kSlotsA)) % WTN >= WTN / 2) lds_dma_16(rsrc_up, to, from);
+    else lds_dma_16(rsrc_b, to, from);
+  };
+
+  // fragment addresses of this lane within a stage, in K-step 0
+  const int fr = lane & 31, fh = lane >> 5;
+  uint32_t a_at[A_ACROSS ? TM : 1], b_at[B_ACROSS ? TN : 1];
+  auto across_at = [&](int bx, int block, int shift) {   // block: of 32 columns
+    const int i = lane & 15, k = 32 * fh + (i >> 2);
+    return (uint32_t)(k * 2 * bx + (((2 * block) ^ shift) + ((lane >> 4) & 1)) * 32 + 8 * (i & 3));
+  };
+  if constexpr (A_ACROSS) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i) a_at[i] = smem_lds + across_at(BM, wm * TM + i, across_shift<BM>((lane & 15) >> 2));
+  } else {
+    a_at[0] = 0;
+  }
+  if constexpr (B_ACROSS) {
+#pragma unroll
+    for (int j = 0; j < TN; ++j) b_at[j] = smem_lds + BM * 128 + across_at(BN, wn * TN + j, across_shift<BN>((lane & 15) >> 2));
+  } else {
+    b_at[0] = 0;
+  }
+
+  i32x4 fa[2][TM], fb[2][TN];
+  f32x16 acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+
+  auto read_across = [&](uint32_t at, int bx) {
+    const u32x2 lo = lds_read_transposed16(at), hi = lds_read_transposed16(at + 8 * bx);
+    return i32x4{(int)lo.x, (int)lo.y, (int)hi.x, (int)hi.y};
+  };
+  auto read_frags = [&](int slot, int kk, int dst) __attribute__((always_inline)) {
+    const uint8_t* base = smem + slot * kStage + Layout::off(fr, 4 * fh + kk);
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      if constexpr (A_ACROSS) fa[dst][i] = read_across(a_at[i] + slot * kStage + kk * 16 * BM, BM);
+      else fa[dst][i] = *(const i32x4*)(base + (wm * TM + i) * 4096);
+    }
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      if constexpr (B_ACROSS) fb[dst][j] = read_across(b_at[j] + slot * kStage + kk * 16 * BN, BN);
+      else fb[dst][j] = *(const i32x4*)(base + BM * 128 + (wn * TN + j) * 4096);
+    }
+  };
+  constexpr int kMfma = TM * TN, kSplit = kMfma > 1 ? kMfma / 2 : 1;
+  constexpr int kReads = TM * (A_ACROSS ? 2 : 1) + TN * (B_ACROSS ? 2 : 1);
+  auto compute = [&](int src, int first, int last) __attribute__((always_inline)) {
+#pragma unroll
+    for (int x = 0; x < kMfma; ++x) {
+      if (x < first || x >= last) continue;
+      acc[x / TN][x % TN] = mfma32<T>(fa[src][x / TN], fb[src][x % TN], acc[x / TN][x % TN]);
+    }
+  };
+  auto interleave = [&](int mfmas, int reads) __attribute__((always_inline)) {
+#pragma unroll
+    for (int x = 0; x < kMfma; ++x) {
+      if (x >= mfmas) break;
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                      // MFMA
+      if (x * kReads < reads * kMfma) __builtin_amdgcn_sched_group_barrier(0x100, (kReads + kMfma - 1) / kMfma, 0);   // DS read
+    }
+  };
+  constexpr int kLoadSteps = 2, kLoadsPerStep = (kSlots + kLoadSteps - 1) / kLoadSteps;
+
+  if (s_begin < s_end) {
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s) {
+      enter_stage(s_begin + s);
+#pragma unroll
+      for (int t = 0; t < kSlots; ++t) issue_load(t, s_begin + s, s);
+    }
+    wait_vmcnt<kInFlight>();
+    block_barrier();
+    read_frags(0, 0, 0);
+    int slot = 0;
+    for (int s = s_begin; s < s_end; ++s) {
+      const int sl = s + STAGES - 1;   // (past the last stage the loads move no data)
+      const int slot_l = slot == 0 ? STAGES - 1 : slot - 1, slot_n = slot == STAGES - 1 ? 0 : slot + 1;
+      enter_stage(sl);
+      auto step = [&](auto kk_c) __attribute__((always_inline)) {
+        constexpr int kk = decltype(kk_c)::value;
+        constexpr int src = kk & 1, dst = src ^ 1;
+        int pre = 0;
+        if constexpr (kk < kLoadSteps) {
+#pragma unroll
+          for (int t = 0; t < kSlots; ++t) {
+            if (t / kLoadsPerStep != kk) continue;
+            if (pre < kMfma) {
+              compute(src, pre, pre + 1);
+              ++pre;
+              __builtin_amdgcn_sched_barrier(0);
+            }
+            issue_load(t, sl, slot_l);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        }
+        if constexpr (kk < 3) {
+          read_frags(slot, kk + 1, dst);
+          compute(src, pre, kMfma);
+          interleave(kMfma - pre, kReads);
+        } else {
+          compute(src, 0, kSplit);
+          interleave(kSplit, 0);
+          __builtin_amdgcn_sched_barrier(0);
+          wait_vmcnt<kInFlight>();   // own loads of stage s + 1 landed
+          wait_lgkmcnt0();           // own reads of stage s done
+          block_barrier();           // ... everyone's
+          read_frags(slot_n, 0, dst);
+          compute(src, kSplit, kMfma);
+          interleave(kMfma - kSplit, kReads);
+        }
+      };
+      step(std::integral_constant<int, 0>());
+      step(std::integral_constant<int, 1>());
+      step(std::integral_constant<int, 2>());
+      step(std::integral_constant<int, 3>());
+      slot = slot_n;
+    }
+  }
+
+  // Every outstanding load (all past the last stage) lands before LDS is
+  // reused, and every wave is done reading; then each wave turns kEpiRows rows
+  // of its part at a time through LDS, so that a lane holds 8 consecutive
+  // columns of one row.
+  wait_vmcnt<0>();
+  wait_lgkmcnt0();
+  block_barrier();
+  uint8_t* const stage_out = smem + wave * kEpiWave;
+  constexpr int kWaveColumns = GATED ? WTN / 2 : WTN;
+  constexpr int kLanesPerRow = kWaveColumns / 8, kRowsPerStore = 64 / kLanesPerRow;
+  const int c = (lane % kLanesPerRow) * 8, col = n0 + wn * kWaveColumns + c;
+#pragma unroll
+  for (int pass = 0; pass < WTM / kEpiRows; ++pass) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int rg = i * 32 + 8 * (e >> 2);
+          if (rg / kEpiRows != pass) continue;
+          *(float*)(stage_out + (rg - pass * kEpiRows + 4 * fh + (e & 3)) * kEpiPitch + (j * 32 + fr) * 4) = acc[i][j][e];
+        }
+    wait_lgkmcnt0();   // this wave's LDS writes done
+    auto staged = [&](int r, int at, float (&v)[8]) {
+      const f32x4 a = *(const f32x4*)(stage_out + r * kEpiPitch + at * 4), b = *(const f32x4*)(stage_out + r * kEpiPitch + at * 4 + 16);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = a[e], v[4 + e] = b[e];
+    };
+#pragma unroll
+    for (int r0 = 0; r0 < kEpiRows; r0 += kRowsPerStore) {
+      const int r = r0 + lane / kLanesPerRow;
+      const int row = m0 + wm * WTM + pass * kEpiRows + r;
+      float v[8], u[8] = {};
+      staged(r, c, v);
+      if constexpr (GATED) staged(r, c + WTN / 2, u);
+      if (row < p.M && col < columns) {
+        if (p.splits > 1) {
+          f32x4* part = (f32x4*)(p.part + ((size_t)blockIdx.y * p.M + row) * p.N + col);
+          part[0] = f32x4{v[0], v[1], v[2], v[3]};
+          part[1] = f32x4{v[4], v[5], v[6], v[7]};
+          if constexpr (GATED) {
+            part = (f32x4*)((float*)part + p.F);
+            part[0] = f32x4{u[0], u[1], u[2], u[3]};
+            part[1] = f32x4{u[4], u[5], u[6], u[7]};
+          }
+        } else {
+          finish8<T, END>(p, row, col, v, u);
+        }
+      }
+    }
+    wait_lgkmcnt0();   // reads done before the next pass overwrites them
+  }
+}
+
+}  // namespace lpgemm

@@ -1,0 +1,7 @@
+// Products of the gated feed-forward block, bf16 operands.
+#define LPGEMM_FFN_DEFINE
+#include "ffn.hpp"
+
+namespace lpgemm {
+template lpgemm_status run_tile<TypeBF16>(int, TileArgs, float*, int, hipStream_t);
+}

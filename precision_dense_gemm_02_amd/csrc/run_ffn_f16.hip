@@ -1,0 +1,7 @@
+// Products of the gated feed-forward block, f16 operands.
+#define LPGEMM_FFN_DEFINE
+#include "ffn.hpp"
+
+namespace lpgemm {
+template lpgemm_status run_tile<TypeF16>(int, TileArgs, float*, int, hipStream_t);
+}

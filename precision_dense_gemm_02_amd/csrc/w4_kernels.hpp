@@ -1,0 +1,105 @@
+// 4-bit weights with group scales: quantisation and its inverse.
+#pragma once
+
+#include "half_types.hpp"
+
+namespace lpgemm {
+
+struct QuantW4Args {
+  const uint8_t* W;
+  uint8_t* codes;
+  uint16_t* scales;
+  uint16_t* zeros;     // null: none
+  int64_t w_stride;    // bytes
+  uint32_t chunks;     // chunks of 8 values per row
+  uint32_t total;      // ... in all rows
+};
+
+// A lane holds 8 values; LANES lanes a group.  The quotients are those of the
+// division, from one reciprocal per group: with r = RN(1 / s) and q = RN(w r),
+// RN(q + r (w - q s)) is the correctly rounded quotient (Markstein), three
+// operations instead of ten.
+template <typename T, int LANES, bool ZEROS>
+__global__ __launch_bounds__(256) void quantize_w4_kernel(QuantW4Args p) {
+  const uint32_t i = blockIdx.x * 256u + threadIdx.x;
+  if (i >= p.total) return;   // (whole groups: rows are whole groups)
+  const uint32_t row = i / p.chunks, chunk = i - row * p.chunks;
+  const i32x4 raw = *(const i32x4*)(p.W + row * p.w_stride + 16 * (int64_t)chunk);
+  const f32x8 w = widen<T>(raw);
+  uint32_t top = 0;            // largest magnitude, as bits: a NaN is larger than everything
+  float lo = 0.f, hi = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float v = w[e];   // (a bit cast of a vector's element would take the first)
+    top = max(top, __builtin_bit_cast(uint32_t, v) & 0x7FFFFFFFu);
+    if constexpr (ZEROS) {
+      lo = fminf(lo, v);
+      hi = fmaxf(hi, v);
+    }
+  }
+#pragma unroll
+  for (int off = 1; off < LANES; off <<= 1) {
+    top = max(top, (uint32_t)__shfl_xor((int)top, off));
+    if constexpr (ZEROS) {
+      lo = fminf(lo, __shfl_xor(lo, off));
+      hi = fmaxf(hi, __shfl_xor(hi, off));
+    }
+  }
+  const bool finite = top < kInfBits;
+  const float span = ZEROS ? hi - lo : __builtin_bit_cast(float, top);
+  uint16_t sbits = finite ? narrow1<T>(span >= kTinyRow ? span / (ZEROS ? 15.f : 7.f) : 0.f) : narrow1<T>(__builtin_nanf(""));
+  const float s = widen1<T>(sbits);
+  const bool live = finite && s > 0.f && s < __builtin_inff();
+  const float r = live ? 1.f / s : 0.f;
+  auto steps = [&](float v) {
+    const float q = __fmul_rn(v, r);
+    return __builtin_rintf(__builtin_fmaf(__builtin_fmaf(-q, s, v), r, q));
+  };
+  const float zero = ZEROS && live ? fminf(fmaxf(-8.f - steps(lo), -8.f), 7.f) : 0.f;
+  uint32_t packed = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float code = live ? fminf(fmaxf(steps(w[e]) + zero, -8.f), 7.f) : 0.f;
+    packed |= ((uint32_t)(int)code & 15u) << (4 * e);
+  }
+  *(uint32_t*)(p.codes + 4 * (int64_t)i) = packed;
+  if (threadIdx.x % LANES == 0) {
+    const uint32_t group = i / LANES;
+    p.scales[group] = sbits;
+    if constexpr (ZEROS) p.zeros[group] = narrow1<T>(zero);
+  }
+}
+
+struct DequantW4Args {
+  const uint8_t* codes;
+  const uint16_t* scales;
+  const uint16_t* zeros;   // null: none
+  uint8_t* Y;
+  uint32_t total;          // chunks of 8 values
+  int lanes_log2;          // chunks per group
+};
+
+// A lane turns 8 codes (4 bytes) into 8 values.  OUT: lpgemm_type of Y.
+template <typename T, int OUT>
+__global__ __launch_bounds__(256) void dequantize_w4_kernel(DequantW4Args p) {
+  const uint32_t i = blockIdx.x * 256u + threadIdx.x;
+  if (i >= p.total) return;
+  const uint32_t packed = *(const uint32_t*)(p.codes + 4 * (int64_t)i);
+  const uint32_t group = i >> p.lanes_log2;
+  const float s = widen1<T>(p.scales[group]);
+  const float z = p.zeros ? widen1<T>(p.zeros[group]) : 0.f;
+  float v[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = __fmul_rn((float)((int)(packed << (28 - 4 * e)) >> 28) - z, s);
+  if constexpr (OUT == 0) {
+    f32x4* y = (f32x4*)(p.Y + 32 * (int64_t)i);
+    y[0] = f32x4{v[0], v[1], v[2], v[3]};
+    y[1] = f32x4{v[4], v[5], v[6], v[7]};
+  } else if constexpr (OUT == 1) {
+    *(i32x4*)(p.Y + 16 * (int64_t)i) = narrow8<TypeF16>(v);
+  } else {
+    *(i32x4*)(p.Y + 16 * (int64_t)i) = narrow8<TypeBF16>(v);
+  }
+}
+
+}  // namespace lpgemm
