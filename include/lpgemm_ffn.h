@@ -90,8 +90,9 @@ lpgemm_status lpgemm_dequantize_w4(int64_t N, int64_t K, int64_t group, lpgemm_t
  * bytes (0 up to LPGEMM_W4_SHORT_M rows; -1 for sizes out of range);
  * INVALID_VALUE where it is missing or too small. */
 #define LPGEMM_MAX_STRIDE 2097152
-#define LPGEMM_W4_SHORT_M 64
-int64_t lpgemm_w4_workspace(int64_t M, int64_t K, int64_t group);
+#define LPGEMM_W4_SHORT_M 4
+#define LPGEMM_W4_EXACT_M 384
+int64_t lpgemm_w4_workspace(int64_t M, int64_t N, int64_t K, int64_t group, int gated);
 lpgemm_status lpgemm_w4(int64_t M, int64_t N, int64_t K, int64_t group, lpgemm_type type, const void *X,
                         int64_t x_stride, const uint8_t *codes, const void *scales, const void *zeros,
                         lpgemm_type out_type, void *C, void *workspace, int64_t workspace_bytes,

@@ -17,6 +17,7 @@ from ._binding import load_library
 from ._moe import _F32, _HALF, _TYPE, _U8, _call, _empty, _f32, _full, _i64, _int, _operand, _out, _out_dtype, _p, _refuse, _rows  # noqa: F401
 
 GROUPS = (32, 64, 128, 256)
+W4_SHORT_M = 4          # up to this many rows the products with 4-bit weights need no workspace
 _ACTIVATION = {"silu": 0, "gelu": 1}
 
 _SIGNATURES = {
@@ -37,10 +38,18 @@ def _size(name: str, *args) -> int:
     f = _sizes.get(name)
     if f is None:
         f = getattr(load_library(), name)
-        f.argtypes = [_i64] * len(args)
+        f.argtypes = [_i64] * 4 + [_int] if name == "lpgemm_w4_workspace" else [_i64] * 3
         f.restype = _i64
         _sizes[name] = f
     return f(*args)
+
+
+def _size_on(dev, name: str, *args) -> int:
+    """A workspace's size on that device; 0 for sizes the call itself will refuse."""
+    if dev.index == torch.cuda.current_device():
+        return max(_size(name, *args), 0)
+    with torch.cuda.device(dev):
+        return max(_size(name, *args), 0)
 
 
 def _activation(name) -> int:
@@ -128,6 +137,12 @@ def _scratch(bytes_needed: int, dev, workspace):
     return workspace.data_ptr(), workspace.numel(), workspace
 
 
+def _w4_scratch(M, N, K, group, gated, dev, workspace):
+    if M <= W4_SHORT_M:
+        return None, 0, None
+    return _scratch(_size_on(dev, "lpgemm_w4_workspace", M, N, K, group, gated), dev, workspace)
+
+
 def gemm_w4(x, codes, scales, zeros: Optional[torch.Tensor] = None, out_dtype=None, out=None, workspace=None):
     """C = x . W^T for 4-bit weights W (N x K, as quantize_w4 makes them) and x,
     M x K fp16 or bf16 of the scales' type (contiguous rows, a row stride that is
@@ -138,7 +153,7 @@ def gemm_w4(x, codes, scales, zeros: Optional[torch.Tensor] = None, out_dtype=No
     dev, t = x.device, x.dtype
     out_dtype = t if out_dtype is None else _out_dtype(out_dtype)
     out = _out(out, "out", (M, N), out_dtype, dev)
-    ws, ws_bytes, _alive = _scratch(_size("lpgemm_w4_workspace", M, K, group) if M > 64 else 0, dev, workspace)
+    ws, ws_bytes, _alive = _w4_scratch(M, N, K, group, 0, dev, workspace)
     _call("lpgemm_w4", dev, M, N, K, group, _HALF[t], x.data_ptr(), stride, codes.data_ptr(), scales.data_ptr(), z,
           _TYPE[out_dtype], out.data_ptr(), ws, ws_bytes)
     return out
@@ -156,7 +171,7 @@ def gated_gemm_w4(x, codes, scales, zeros: Optional[torch.Tensor] = None, activa
     dev, t, F = x.device, x.dtype, N // 2
     out_dtype = t if out_dtype is None else _out_dtype(out_dtype)
     out = _out(out, "out", (M, F), out_dtype, dev)
-    ws, ws_bytes, _alive = _scratch(_size("lpgemm_w4_workspace", M, K, group) if M > 64 else 0, dev, workspace)
+    ws, ws_bytes, _alive = _w4_scratch(M, N, K, group, 1, dev, workspace)
     _call("lpgemm_gated_w4", dev, M, F, K, group, _HALF[t], act, x.data_ptr(), stride, codes.data_ptr(),
           scales.data_ptr(), z, _TYPE[out_dtype], out.data_ptr(), ws, ws_bytes)
     return out
@@ -186,15 +201,6 @@ def _block(x, w_gate_up, w_down):
     return M, D, F, stride
 
 
-def _workspace_of(name, M, D, F, dev, workspace):
-    if dev.index == torch.cuda.current_device():
-        need = _size(name, M, D, F)
-    else:
-        with torch.cuda.device(dev):
-            need = _size(name, M, D, F)
-    return _scratch(max(need, 0), dev, workspace)
-
-
 def gated_ffn(x, w_gate_up, w_down, activation: str = "silu", keep: bool = False, out=None, gate_up_out=None,
               workspace=None):
     """The gated feed-forward block (act(x . G^T) * (x . U^T)) . w_down^T.
@@ -212,7 +218,7 @@ def gated_ffn(x, w_gate_up, w_down, activation: str = "silu", keep: bool = False
         raise ValueError("gate_up_out goes with keep=True")
     out = _out(out, "out", (M, D), t, dev)
     gate_up = _out(gate_up_out, "gate_up_out", (M, 2 * F), t, dev) if keep else None
-    ws, ws_bytes, _alive = _workspace_of("lpgemm_gated_ffn_workspace", M, D, F, dev, workspace)
+    ws, ws_bytes, _alive = _scratch(_size_on(dev, "lpgemm_gated_ffn_workspace", M, D, F), dev, workspace)
     _call("lpgemm_gated_ffn", dev, M, D, F, _HALF[t], act, x.data_ptr(), stride, w_gate_up.data_ptr(),
           w_down.data_ptr(), gate_up.data_ptr() if keep else None, out.data_ptr(), ws, ws_bytes)
     return (out, gate_up) if keep else out
@@ -240,7 +246,7 @@ def gated_ffn_backward(dy, x, w_gate_up, w_down, gate_up, activation: str = "sil
     if len(needs) != 3:
         raise ValueError("needs must say which of dx, dw_gate_up and dw_down are wanted")
     grads = [_empty(*s, dtype=d, device=dev) if n else None for n, (s, d) in zip(needs, shapes)]
-    ws, ws_bytes, _alive = _workspace_of("lpgemm_gated_ffn_backward_workspace", M, D, F, dev, workspace)
+    ws, ws_bytes, _alive = _scratch(_size_on(dev, "lpgemm_gated_ffn_backward_workspace", M, D, F), dev, workspace)
     _call("lpgemm_gated_ffn_backward", dev, M, D, F, _HALF[t], act, dy.data_ptr(), dy_stride, x.data_ptr(), stride,
           w_gate_up.data_ptr(), w_down.data_ptr(), gate_up.data_ptr(), _TYPE[grad_dtype],
           *[g.data_ptr() if g is not None else None for g in grads], ws, ws_bytes)

@@ -19,6 +19,7 @@ struct FewRowsArgs {
   int F;                    // gated: N / 2, else 0
   int activation;
   int x_stride;             // bytes
+  int x_lds_stride;         // XLDS: bytes of a row of X in LDS
   int row_bytes;            // of W
   int groups;               // scales of a row
   int group_shift;          // 4 bits, groups of 128 and more: log2 of a group's blocks
@@ -58,12 +59,9 @@ __device__ __forceinline__ void store_value(uint8_t* C, int out_type, size_t i, 
   else ((uint16_t*)C)[i] = out_type == 1 ? narrow1<TypeF16>(v) : narrow1<TypeBF16>(v);
 }
 
-// The most wavefronts of a workgroup: registers bound it.
-constexpr int few_rows_waves(int mt, int nb) { return mt * nb == 1 ? 16 : mt * nb == 8 ? 4 : 8; }
-
 // MT x 16 rows of X against NB x 16 rows of W per workgroup, whose waves take
-// the blocks of 128 k in turn; their sums meet in LDS and are added in the
-// waves' order.
+// runs of blocks of 128 k in turn, with DEPTH of them in flight; their sums meet in LDS and are
+// added in the waves' order.
 //
 // A lane loads 16 bytes of a weight row.  16-bit weights: 8 values of k, and
 // four loads make a block.  4 bits: 32 values, a quarter of a block; the four
@@ -73,14 +71,22 @@ constexpr int few_rows_waves(int mt, int nb) { return mt * nb == 1 ? 16 : mt * n
 // 4 bits: the codes enter the matrix instruction as 24 + code (one or two
 // operations per pair), the sum of x comes from a product with ones, and
 //   C += scale * (sum x (24 + code) - (24 + zero) sum x)
-// per group, in binary32.
+// per group, in binary32.  The four lanes of a row load the scales of a block's
+// groups and hand them round.
+//
+// Whole blocks need no check of k: a lane's offset stays, the descriptors'
+// bases move.
 //
 // W4: 0 for 16-bit weights, else the K-steps of 32 that share a scale (1, 2,
-// or 4 for groups of 128 and more).
-template <typename T, int W4, int MT, int NB>
-__global__ __launch_bounds__(64 * few_rows_waves(MT, NB)) void few_rows(FewRowsArgs p) {
-  constexpr int kSub = W4 ? 4 / W4 : 1;       // groups in a block
-  constexpr int kLoads = W4 ? 1 : 4;          // 16-byte loads per weight row and block
+// or 4 for groups of 128 and more).  XLDS: X, a few rows of it, is copied into
+// LDS first, where its fragments cost no vector loads.
+template <typename T, int W4, bool ZEROS, int MT, int NB, bool XLDS, int WAVES, int DEPTH>
+__global__ __launch_bounds__(64 * WAVES) void few_rows(FewRowsArgs p) {
+  static_assert(!XLDS || MT == 1, "a few rows");
+  constexpr int kSub = W4 ? 4 / W4 : 1;                 // groups in a block
+  constexpr int kLoads = W4 ? 1 : 4;                    // 16-byte loads per weight row and block
+  constexpr int RUN = W4 ? 2 : 1;                       // consecutive blocks a wave takes: whole cache lines of a row
+  constexpr int kScaleLoads = W4 == 1 ? 2 : 1;          // per row and run, four groups each
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int waves = blockDim.x >> 6;
   const int r = lane & 15, q = lane >> 4;
@@ -89,74 +95,135 @@ __global__ __launch_bounds__(64 * few_rows_waves(MT, NB)) void few_rows(FewRowsA
   const int per_half = gated ? NB / 2 : NB;   // column tiles of 16 per projection
   const int c0 = blockIdx.x * (16 * per_half);
   const int columns = gated ? p.F : p.N;
-  const int blocks = (p.K + 127) >> 7;
+  const int blocks = (p.K + 127) >> 7, whole = p.K >> 7;
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
 
   const int rows_x = min(16 * MT, p.M - m0);
-  const auto rsrc_x = __builtin_amdgcn_make_buffer_rsrc((void*)(p.X + (size_t)m0 * p.x_stride), 0,
-                                                        rows_x * p.x_stride, kBufferWord3);
-  // first weight row of column tile nb, and how many there are
+  const uint8_t* const x_base = p.X + (size_t)m0 * p.x_stride;
+  // a column tile's weight rows: the first, and how many
   auto first_row = [&](int nb) { return nb < per_half ? c0 + 16 * nb : p.F + c0 + 16 * (nb - per_half); };
   auto row_count = [&](int nb) { return max(min(columns - (c0 + 16 * (nb < per_half ? nb : nb - per_half)), 16), 0); };
+  const uint8_t* w_base[NB];
+  const uint8_t *s_base[NB], *z_base[NB];
+  uint32_t w_off[NB], s_off[NB];              // this lane's, in block 0
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    const size_t row = first_row(nb);
+    w_base[nb] = p.W + row * p.row_bytes;
+    s_base[nb] = (const uint8_t*)(p.scales + row * p.groups);
+    z_base[nb] = (const uint8_t*)(p.zeros + row * p.groups);
+    const bool row_here = r < row_count(nb);
+    w_off[nb] = row_here ? (uint32_t)(r * p.row_bytes + 16 * q) : kOutOfRange;
+    const int g = W4 == 4 ? (q & 1) >> p.group_shift : q;   // (groups past a row's last: of blocks that are not whole, unused)
+    s_off[nb] = row_here ? 2u * (r * p.groups + g) : kOutOfRange;
+  }
+  uint32_t x_off[MT];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) x_off[mt] = 16 * mt + r < rows_x ? (uint32_t)((16 * mt + r) * p.x_stride + 16 * q) : kOutOfRange;
+  auto rsrc_of = [](const void* base, int bytes = 0x7FFFFFFF) { return __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, bytes, kBufferWord3); };
 
-  struct Block {
-    i32x4 w[NB][kLoads];
-    i32x4 x[MT][4];
-    uint16_t s[NB][kSub], z[NB][kSub];
+  struct Run {
+    i32x4 w[RUN][NB][kLoads];
+    i32x4 x[XLDS ? 1 : RUN][MT][4];
+    uint16_t s[NB][kScaleLoads], z[NB][kScaleLoads];   // of group q of the load
   };
-  auto load = [&](Block& b, int kb) {
+  // a run of whole blocks, or (past the last) zeros: the loads go out in any
+  // case, so that a wait on one leaves those behind it in flight
+  const int runs = (whole + RUN - 1) / RUN;
+  const int first_run = runs > 0 ? (int)(blockIdx.x * 5u % (uint32_t)runs) : 0;
+  auto place = [&](int i) { const int run = i + first_run; return i >= runs ? whole : run >= runs ? run - runs : run; };
+  auto load = [&](Run& b, int i) __attribute__((always_inline)) {
+    const int run = place(i);
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      const int row = first_row(nb), count = row_count(nb);
-      const auto rsrc_w = __builtin_amdgcn_make_buffer_rsrc((void*)(p.W + (size_t)row * p.row_bytes), 0,
-                                                            count * p.row_bytes, kBufferWord3);
+    for (int h = 0; h < RUN; ++h) {
+      const int kb = run * RUN + h;
+      const int bytes = kb < whole ? 0x7FFFFFFF : 0;
 #pragma unroll
-      for (int l = 0; l < kLoads; ++l) {
-        const int at = W4 ? kb * 64 + 16 * q : kb * 256 + 64 * l + 16 * q;
-        b.w[nb][l] = __builtin_amdgcn_raw_buffer_load_b128(rsrc_w, at < p.row_bytes ? r * p.row_bytes + at : kOutOfRange, 0, 0);
+      for (int nb = 0; nb < NB; ++nb) {
+        const auto rsrc = rsrc_of(w_base[nb] + (size_t)kb * (W4 ? 64 : 256), bytes);
+#pragma unroll
+        for (int l = 0; l < kLoads; ++l) b.w[h][nb][l] = __builtin_amdgcn_raw_buffer_load_b128(rsrc, w_off[nb] + 64 * l, 0, 0);
       }
-      if constexpr (W4 != 0) {
-        const size_t g0 = (size_t)row * p.groups;
-        const auto rsrc_s = __builtin_amdgcn_make_buffer_rsrc((void*)(p.scales + g0), 0, count * p.groups * 2, kBufferWord3);
-        const auto rsrc_z = __builtin_amdgcn_make_buffer_rsrc((void*)(p.zeros ? p.zeros + g0 : p.scales), 0,
-                                                              p.zeros ? count * p.groups * 2 : 0, kBufferWord3);
+    }
+    if constexpr (!XLDS) {
 #pragma unroll
-        for (int t = 0; t < kSub; ++t) {
-          const int g = W4 == 4 ? kb >> p.group_shift : kb * kSub + t;
-          const uint32_t off = g < p.groups ? 2 * (r * p.groups + g) : kOutOfRange;
-          b.s[nb][t] = __builtin_amdgcn_raw_buffer_load_b16(rsrc_s, off, 0, 0);
-          b.z[nb][t] = __builtin_amdgcn_raw_buffer_load_b16(rsrc_z, off, 0, 0);
+      for (int h = 0; h < RUN; ++h) {
+        const int kb = run * RUN + h;
+        const auto rsrc = rsrc_of(x_base + (size_t)kb * 256, kb < whole ? 0x7FFFFFFF : 0);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) b.x[h][mt][j] = __builtin_amdgcn_raw_buffer_load_b128(rsrc, x_off[mt] + 64 * j, 0, 0);
+      }
+    }
+    if constexpr (W4 != 0) {
+#pragma unroll
+      for (int t = 0; t < kScaleLoads; ++t) {
+        // groups of 32: those of block t of the run; of 64: two of each block; more: one of each (both may be the same)
+        const int g = W4 == 4 ? (run * 2) >> p.group_shift : W4 == 2 ? run * 4 : (run * 2 + t) * 4;
+        const int bytes = run * 2 < whole ? 0x7FFFFFFF : 0;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          b.s[nb][t] = __builtin_amdgcn_raw_buffer_load_b16(rsrc_of(s_base[nb] + 2 * (size_t)g, bytes), s_off[nb], 0, 0);
+          b.z[nb][t] = ZEROS ? __builtin_amdgcn_raw_buffer_load_b16(rsrc_of(z_base[nb] + 2 * (size_t)g, bytes), s_off[nb], 0, 0) : 0;
         }
       }
     }
+  };
+  // the last block, where the row ends inside it
+  auto load_end = [&](Run& b) __attribute__((always_inline)) {
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int k = kb * 128 + 32 * j + 8 * q;
-        b.x[mt][j] = __builtin_amdgcn_raw_buffer_load_b128(rsrc_x, k < p.K ? (16 * mt + r) * p.x_stride + 2 * k : kOutOfRange, 0, 0);
+      for (int l = 0; l < kLoads; ++l) {
+        const int at = W4 ? whole * 64 : whole * 256 + 64 * l;
+        b.w[0][nb][l] = __builtin_amdgcn_raw_buffer_load_b128(rsrc_of(w_base[nb]), at + 16 * q < p.row_bytes ? w_off[nb] + at : kOutOfRange, 0, 0);
       }
+      if constexpr (W4 != 0) {
+        const int g = W4 == 4 ? whole >> p.group_shift : whole * kSub;
+        const int own = W4 == 4 ? 0 : W4 == 2 ? q & 1 : q;
+        const uint32_t off = g + own < p.groups && w_off[nb] != kOutOfRange ? 2u * (r * p.groups + g + own) : kOutOfRange;
+        b.s[nb][0] = __builtin_amdgcn_raw_buffer_load_b16(rsrc_of(s_base[nb]), off, 0, 0);
+        b.z[nb][0] = ZEROS ? __builtin_amdgcn_raw_buffer_load_b16(rsrc_of(z_base[nb]), off, 0, 0) : 0;
+      }
+    }
+    if constexpr (!XLDS) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int at = whole * 128 + 32 * j;
+          b.x[0][mt][j] = __builtin_amdgcn_raw_buffer_load_b128(rsrc_of(x_base), at + 8 * q < p.K ? x_off[mt] + 2 * at : kOutOfRange, 0, 0);
+        }
+    }
   };
 
   f32x4 acc[MT][NB] = {};
-  auto compute = [&](const Block& b) {
+  auto compute = [&](const Run& b, int h, int kb) __attribute__((always_inline)) {   // block h of the run
+    i32x4 x[MT][4];
+    if constexpr (XLDS) {
+      const uint8_t* at = smem + min(r, rows_x - 1) * p.x_lds_stride + kb * 256 + 16 * q;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[0][j] = *(const i32x4*)(at + 64 * j);
+    } else {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[mt][j] = W4 ? code_order(b.x[h][mt][j]) : b.x[h][mt][j];
+    }
     if constexpr (W4 == 0) {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) acc[mt][nb] = mfma16<T>(b.x[mt][j], b.w[nb][j], acc[mt][nb]);
+          for (int nb = 0; nb < NB; ++nb) acc[mt][nb] = mfma16<T>(x[mt][j], b.w[h][nb][j], acc[mt][nb]);
     } else {
       const int one = kIsF16<T> ? 0x3C003C00 : 0x3F803F80;
       const i32x4 ones = {one, one, one, one};
-      i32x4 x[MT][4];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x[mt][j] = code_order(b.x[mt][j]);
       u32x4 w[NB];
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) w[nb] = transpose_rows(__builtin_bit_cast(u32x4, b.w[nb][0]));
+      for (int nb = 0; nb < NB; ++nb) w[nb] = transpose_rows(__builtin_bit_cast(u32x4, b.w[h][nb][0]));
 #pragma unroll
       for (int t = 0; t < kSub; ++t) {
         f32x4 sum[MT] = {}, part[MT][NB] = {};
@@ -166,14 +233,17 @@ __global__ __launch_bounds__(64 * few_rows_waves(MT, NB)) void few_rows(FewRowsA
           for (int mt = 0; mt < MT; ++mt) sum[mt] = mfma16<T>(x[mt][j], ones, sum[mt]);
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
-            const i32x4 f = code_fragment<T>(w[nb][j]);
+            const uint32_t word = w[nb][j];
+            const i32x4 f = code_fragment<T>(word);
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) part[mt][nb] = mfma16<T>(x[mt][j], f, part[mt][nb]);
           }
         }
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-          const float s = widen1<T>(b.s[nb][t]), z = -kCodeBias - widen1<T>(b.z[nb][t]);
+          const int at = W4 == 1 ? h : 0, from = W4 == 1 ? t : W4 == 2 ? 2 * h + t : h;   // the load, and the lane row that holds the group
+          const uint32_t sz = __shfl((int)(b.s[nb][at] | (uint32_t)b.z[nb][at] << 16), 16 * from + r);
+          const float s = widen1<T>((uint16_t)sz), z = -kCodeBias - widen1<T>((uint16_t)(sz >> 16));
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -184,21 +254,54 @@ __global__ __launch_bounds__(64 * few_rows_waves(MT, NB)) void few_rows(FewRowsA
     }
   };
 
-  if (wave < blocks) {
-    Block b0, b1;
-    load(b0, wave);
-    int kb = wave;
-    for (; kb + waves < blocks; kb += 2 * waves) {
-      load(b1, kb + waves);
-      compute(b0);
-      load(b0, kb + 2 * waves);   // (past the end: zeros, unused)
-      compute(b1);
+  {
+    // X into LDS: rows of whole blocks, zeros behind K, in the order the
+    // fragments need.  Its loads go out before the weights' (the last two of
+    // each thread, which is all of them for one row) and are waited for behind.
+    const int chunks = blocks * 16;
+    auto x_chunk = [&](int i) -> i32x4 {
+      const int row = i / chunks, c = i - row * chunks;
+      return i < rows_x * chunks && 8 * c < p.K ? *(const i32x4*)(x_base + (size_t)row * p.x_stride + 16 * c) : i32x4{0, 0, 0, 0};
+    };
+    auto put_chunk = [&](int i, const i32x4& v) {
+      const int row = i / chunks, c = i - row * chunks;
+      if (i < rows_x * chunks) *(i32x4*)(smem + row * p.x_lds_stride + 16 * c) = W4 ? code_order(v) : v;
+    };
+    const int threads = blockDim.x;
+    i32x4 x0, x1;
+    if constexpr (XLDS) {
+      for (int i = 2 * threads + threadIdx.x; i < rows_x * chunks; i += threads) put_chunk(i, x_chunk(i));
+      x0 = x_chunk(threadIdx.x);
+      x1 = x_chunk(threads + threadIdx.x);
     }
-    if (kb < blocks) compute(b0);
+    Run ring[DEPTH];
+#pragma unroll
+    for (int i = 0; i < DEPTH; ++i) load(ring[i], wave + i * waves);
+    if constexpr (XLDS) {
+      put_chunk(threadIdx.x, x0);
+      put_chunk(threads + threadIdx.x, x1);
+      __syncthreads();
+    }
+    for (int run = wave; run < runs; run += DEPTH * waves) {
+#pragma unroll
+      for (int i = 0; i < DEPTH; ++i) {
+#pragma unroll
+        for (int h = 0; h < RUN; ++h) {
+          const int kb = place(run + i * waves) * RUN + h;
+          if (kb < whole) compute(ring[i], h, kb);
+        }
+        load(ring[i], run + (i + DEPTH) * waves);
+      }
+    }
+    if (whole < blocks && wave == runs % waves) {
+      load_end(ring[0]);
+      compute(ring[0], 0, whole);
+    }
+    if constexpr (XLDS) __syncthreads();
   }
 
+  float* const red = (float*)smem;
   // sums: [wave][row][column], a column more for the banks
-  extern __shared__ __attribute__((aligned(16))) float red[];
   constexpr int kPitch = 16 * NB + 1, kWave = 16 * MT * kPitch;
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt)

@@ -2,6 +2,14 @@
 #include "ffn.hpp"
 #include "few_rows.hpp"
 
+namespace lpgemm {
+int g_tile_bm[5], g_tile_splits[5], g_few_limit = 64;
+int g_few_rows_nb = 0, g_few_rows_waves = 0, g_few_rows_lds = 64;
+}
+extern "C" void lpgemm_tune_tile(int job, int bm, int splits) { lpgemm::g_tile_bm[job] = bm; lpgemm::g_tile_splits[job] = splits; }
+extern "C" void lpgemm_tune_limit(int m) { lpgemm::g_few_limit = m; }
+extern "C" void lpgemm_tune_few_rows(int nb, int waves, int lds) { lpgemm::g_few_rows_nb = nb; lpgemm::g_few_rows_waves = waves; lpgemm::g_few_rows_lds = lds; }
+
 using namespace lpgemm;
 
 namespace {
@@ -28,9 +36,9 @@ struct ForwardSpace {
     h = 0;
     part = round256(2 * M * F);
     int64_t sums = 0;
-    if (M > kFewRows) {
-      const int64_t a = split_bytes(plan_tiles(JOB_GATED, M, 2 * F, D, cu_count), M, 2 * F);
-      const int64_t b = split_bytes(plan_tiles(JOB_DOWN, M, D, F, cu_count), M, D);
+    if (M > g_few_limit) {
+      const int64_t a = split_bytes(plan_tiles(JOB_GATED, M, 2 * F, D, cu_count), JOB_GATED, M, 2 * F);
+      const int64_t b = split_bytes(plan_tiles(JOB_DOWN, M, D, F, cu_count), JOB_DOWN, M, D);
       sums = a > b ? a : b;
     }
     total = part + round256(sums);
@@ -44,7 +52,7 @@ struct BackwardSpace {
     part = h + round256(2 * M * F);
     int64_t sums = 0;
     auto add = [&](int job, int64_t m, int64_t n, int64_t k) {
-      const int64_t b = split_bytes(plan_tiles(job, m, n, k, cu_count), m, n);
+      const int64_t b = split_bytes(plan_tiles(job, m, n, k, cu_count), job, m, n);
       if (b > sums) sums = b;
     };
     add(JOB_GATED_GRAD, M, F, D);
@@ -70,7 +78,7 @@ lpgemm_status forward(int64_t M, int64_t D, int64_t F, int activation, const voi
   const ForwardSpace space(M, D, F, cu_count);
   uint8_t* const h = ws + space.h;
   lpgemm_status st = LPGEMM_SUCCESS;
-  if (M <= kFewRows) {
+  if (M <= g_few_limit) {
     FewRowsArgs p{};
     p.X = static_cast<const uint8_t*>(X);
     p.W = static_cast<const uint8_t*>(w_gate_up);
@@ -104,6 +112,7 @@ lpgemm_status forward(int64_t M, int64_t D, int64_t F, int activation, const voi
   p.b_stride = 2 * D;
   p.H = h;
   p.GU = static_cast<uint8_t*>(GU);
+  p.out_type = kIsF16<T> ? LPGEMM_F16 : LPGEMM_BF16;
   p.activation = activation;
   p.M = (int)M;
   p.N = (int)(2 * F);

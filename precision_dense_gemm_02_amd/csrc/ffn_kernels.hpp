@@ -9,14 +9,14 @@
 #pragma once
 
 #include "activation.hpp"
-#include "half_types.hpp"
+#include "few_rows_kernels.hpp"
 
 namespace lpgemm {
 
 // What becomes of a tile of sums.
 enum TileEnd {
   END_STORE = 0,       // C, in out_type
-  END_GATED = 1,       // columns are pairs gate, up: H = act(gate) * up, and [gate up] if GU is set
+  END_GATED = 1,       // columns are pairs gate, up: H = act(gate) * up in out_type, and [gate up] if GU is set
   END_GATED_GRAD = 2,  // sums are dh: from [gate up] in GU, [dg du] into DGU and h into H
 };
 
@@ -26,7 +26,7 @@ struct TileArgs {
   int64_t a_stride;        // bytes from one stored row to the next
   int64_t b_stride;
   uint8_t* C;              // END_STORE: rows of N values
-  int out_type;            // ... lpgemm_type
+  int out_type;            // lpgemm_type of C (END_GATED: of H)
   uint8_t* H;              // M x F
   uint8_t* GU;             // M x 2 F
   uint8_t* DGU;            // M x 2 F
@@ -36,7 +36,8 @@ struct TileArgs {
   int k_stages;            // K-stages of 64, all of them
   int split_stages;        // ... of one split (blockIdx.y)
   int splits;
-  float* part;             // splits > 1: splits x M x N sums
+  float* part;             // splits > 1: splits x M x part_stride sums (END_GATED: the up projection's in the second half)
+  int part_stride;
   int tiles_m, tiles_n;
 };
 
@@ -49,19 +50,30 @@ __device__ __forceinline__ int across_shift(int k) {
   return COLS >= 128 ? 2 * (k & 3) : 2 * ((k >> 1) & 1);
 }
 
+// Up to eight consecutive values of a row of `columns`, from column `col` on.
+__device__ __forceinline__ void store_columns(uint8_t* C, int out_type, int row, int col, int columns, const float (&v)[8]) {
+  const size_t at = (size_t)row * columns + col;
+  if (columns % 8 == 0) {
+    if (out_type == 0) {
+      f32x4* c = (f32x4*)(C + 4 * at);
+      c[0] = f32x4{v[0], v[1], v[2], v[3]};
+      c[1] = f32x4{v[4], v[5], v[6], v[7]};
+    } else {
+      *(i32x4*)(C + 2 * at) = out_type == 1 ? narrow8<TypeF16>(v) : narrow8<TypeBF16>(v);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (col + e < columns) store_value(C, out_type, at + e, v[e]);
+  }
+}
+
 // Eight consecutive columns of one row: what END does with them.  `v`: the sums
 // (END_GATED: of the gate), `u`: those of the up projection.
 template <typename T, int END>
 __device__ __forceinline__ void finish8(const TileArgs& p, int row, int col, const float (&v)[8], const float (&u)[8]) {
   if constexpr (END == END_STORE) {
-    const size_t at = (size_t)row * p.N + col;
-    if (p.out_type == 0) {
-      f32x4* c = (f32x4*)(p.C + 4 * at);
-      c[0] = f32x4{v[0], v[1], v[2], v[3]};
-      c[1] = f32x4{v[4], v[5], v[6], v[7]};
-    } else {
-      *(i32x4*)(p.C + 2 * at) = narrow8<T>(v);
-    }
+    store_columns(p.C, p.out_type, row, col, p.N, v);
   } else if constexpr (END == END_GATED) {
     float h[8];
 #pragma unroll
@@ -71,7 +83,7 @@ __device__ __forceinline__ void finish8(const TileArgs& p, int row, int col, con
       *(i32x4*)gu = narrow8<T>(v);
       *(i32x4*)(gu + 2 * (size_t)p.F) = narrow8<T>(u);
     }
-    *(i32x4*)(p.H + 2 * ((size_t)row * p.F + col)) = narrow8<T>(h);
+    store_columns(p.H, p.out_type, row, col, p.F, h);
   } else {
     const size_t at = 2 * ((size_t)row * 2 * p.F + col);
     const f32x8 g = widen<T>(*(const i32x4*)(p.GU + at)), up = widen<T>(*(const i32x4*)(p.GU + at + 2 * (size_t)p.F));
@@ -95,19 +107,19 @@ template <typename T, int END>
 __global__ __launch_bounds__(256) void join_splits(TileArgs p) {
   const int columns = END == END_GATED ? p.F : p.N;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int chunks = columns / 8;
+  const int chunks = (columns + 7) / 8;
   const int row = (int)(i / chunks), col = 8 * (int)(i - (int64_t)row * chunks);
   if (row >= p.M) return;
   float v[8] = {}, u[8] = {};
   for (int s = 0; s < p.splits; ++s) {
-    const float* part = p.part + ((size_t)s * p.M + row) * p.N + col;
+    const float* part = p.part + ((size_t)s * p.M + row) * p.part_stride + col;
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       const f32x4 a = *(const f32x4*)(part + 4 * q);
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[4 * q + e] += a[e];
       if constexpr (END == END_GATED) {
-        const f32x4 b = *(const f32x4*)(part + p.F + 4 * q);
+        const f32x4 b = *(const f32x4*)(part + p.part_stride / 2 + 4 * q);
 #pragma unroll
         for (int e = 0; e < 4; ++e) u[4 * q + e] += b[e];
       }
@@ -116,20 +128,20 @@ __global__ __launch_bounds__(256) void join_splits(TileArgs p) {
   finish8<T, END>(p, row, col, v, u);
 }
 
-// BM x BN tiles, four waves in a WM x WN grid, a ring of STAGES K-stages of 64.
-// A stage holds an operand's rows of 128 bytes along k, or its 64 k-rows
+// BM x BN tiles, four waves in a WM x WN grid, rings of SA and SB K-stages of 64
+// for the two operands.  A stage holds an operand's rows of 128 bytes along k, or its 64 k-rows
 // across it; both arrive by 16-byte direct-to-LDS loads, swizzled, and leave
 // as 32 x 16 fragments: one ds_read_b128, or two transposing ds_read_b64.  Lane
 // l has k = 32 (l / 32) + 8 kk .. + 7 of the stage in K-step kk for both.
 //
-// The loads of stage s + STAGES - 1 go out in the first two K-steps of stage s,
-// one matrix instruction pinned in front of each; one barrier per stage, in its
+// The loads of A's stage s + SA - 1 and B's stage s + SB - 1 go out in the first
+// two K-steps of stage s, one matrix instruction pinned in front of each; one barrier per stage, in its
 // last K-step, publishes stage s + 1, whose first fragments are read while the
 // rest of stage s's products run.
 //
 // END_GATED: a wave's columns are WTN / 2 of the gate and the same of the up
 // projection, so that both sums of an element meet in one lane.
-template <typename T, bool A_ACROSS, bool B_ACROSS, int BM, int BN, int WM, int WN, int STAGES, int END>
+template <typename T, bool A_ACROSS, bool B_ACROSS, int BM, int BN, int WM, int WN, int SA, int SB, int END>
 __global__ __launch_bounds__(256) void ffn_tile(TileArgs p) {
   using Layout = RowLayout<128>;
   constexpr int WTM = BM / WM, WTN = BN / WN;
@@ -137,15 +149,20 @@ __global__ __launch_bounds__(256) void ffn_tile(TileArgs p) {
   static_assert(WM * WN == 4 && TM >= 1 && TN >= 1 && WTM % 32 == 0 && WTN % 32 == 0, "wave tiles");
   static_assert(END != END_GATED || (!B_ACROSS && TN % 2 == 0), "gate and up columns in one wave");
   constexpr bool GATED = END == END_GATED;
-  constexpr int kRows = BM + BN, kStage = kRows * 128;
-  constexpr int kSlots = kRows / 32, kSlotsA = BM / 32;   // 1 KiB loads per wave and stage
+  constexpr int kStageA = BM * 128, kStageB = BN * 128, kRingB = SA * kStageA;
+  constexpr int kSlots = (BM + BN) / 32, kSlotsA = BM / 32, kSlotsB = BN / 32;   // 1 KiB loads per wave and stage
   constexpr int kEpiPitch = WTN * 4 + 32;
   constexpr int kEpiRows = WTM < 64 ? WTM : 64;
   constexpr int kEpiWave = kEpiRows * kEpiPitch;
-  constexpr int kLds = STAGES * kStage > 4 * kEpiWave ? STAGES * kStage : 4 * kEpiWave;
+  constexpr int kRings = kRingB + SB * kStageB;
+  constexpr int kLds = kRings > 4 * kEpiWave ? kRings : 4 * kEpiWave;
   static_assert(kLds <= 160 * 1024, "LDS");
-  constexpr int kInFlight = (STAGES - 2) * kSlots;
-  static_assert(STAGES >= 2 && kInFlight + kSlots <= 63, "vmcnt range");
+  // loads that may be in flight once stage s + 1 has landed: those behind the
+  // later of A's and B's, which go out in stages s + 2 - SA and s + 2 - SB, A's
+  // before B's
+  static_assert(SB >= SA && SA >= 2, "rings");
+  constexpr int kInFlight = (SA - 2) * kSlots + (SB > SA ? kSlotsB : 0);
+  static_assert(kInFlight + kSlots <= 63, "vmcnt range");
 
   __shared__ __attribute__((aligned(1024))) uint8_t smem[kLds];
 
@@ -204,13 +221,13 @@ __global__ __launch_bounds__(256) void ffn_tile(TileArgs p) {
     return make_rsrc(base + (int64_t)64 * s * stride, (uint32_t)(left * stride));
   };
   i32x4 rsrc_a = rsrc_a_along, rsrc_b = rsrc_b_along;
-  auto enter_stage = [&](int s) {   // the descriptors for the loads of stage s
-    if constexpr (A_ACROSS) rsrc_a = across_rsrc(a_base, p.a_stride, s);
-    if constexpr (B_ACROSS) rsrc_b = across_rsrc(b_base, p.b_stride, s);
+  auto enter_stage = [&](int sa, int sb) {   // the descriptors for the loads of these stages
+    if constexpr (A_ACROSS) rsrc_a = across_rsrc(a_base, p.a_stride, sa);
+    if constexpr (B_ACROSS) rsrc_b = across_rsrc(b_base, p.b_stride, sb);
   };
-  auto issue_load = [&](int t, int s, int slot) __attribute__((always_inline)) {
+  auto issue_load = [&](int t, int s, int slot) __attribute__((always_inline)) {   // of stage s, into that place of the ring
     const bool is_a = t < kSlotsA;
-    const uint32_t to = smem_lds + slot * kStage + (4 * t + wave) * 1024;
+    const uint32_t to = smem_lds + (is_a ? slot * kStageA + (4 * t + wave) * 1024 : kRingB + slot * kStageB + (4 * (t - kSlotsA) + wave) * 1024);
     uint32_t from = off[t];
     if (!(is_a ? A_ACROSS : B_ACROSS)) {
       const uint32_t kbyte = (uint32_t)s * 128;
@@ -236,7 +253,7 @@ __global__ __launch_bounds__(256) void ffn_tile(TileArgs p) {
   }
   if constexpr (B_ACROSS) {
 #pragma unroll
-    for (int j = 0; j < TN; ++j) b_at[j] = smem_lds + BM * 128 + across_at(BN, wn * TN + j, across_shift<BN>((lane & 15) >> 2));
+    for (int j = 0; j < TN; ++j) b_at[j] = smem_lds + kRingB + across_at(BN, wn * TN + j, across_shift<BN>((lane & 15) >> 2));
   } else {
     b_at[0] = 0;
   }
@@ -254,17 +271,17 @@ __global__ __launch_bounds__(256) void ffn_tile(TileArgs p) {
     const u32x2 lo = lds_read_transposed16(at), hi = lds_read_transposed16(at + 8 * bx);
     return i32x4{(int)lo.x, (int)lo.y, (int)hi.x, (int)hi.y};
   };
-  auto read_frags = [&](int slot, int kk, int dst) __attribute__((always_inline)) {
-    const uint8_t* base = smem + slot * kStage + Layout::off(fr, 4 * fh + kk);
+  auto read_frags = [&](int slot_a, int slot_b, int kk, int dst) __attribute__((always_inline)) {
+    const uint8_t* base = smem + Layout::off(fr, 4 * fh + kk);
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
-      if constexpr (A_ACROSS) fa[dst][i] = read_across(a_at[i] + slot * kStage + kk * 16 * BM, BM);
-      else fa[dst][i] = *(const i32x4*)(base + (wm * TM + i) * 4096);
+      if constexpr (A_ACROSS) fa[dst][i] = read_across(a_at[i] + slot_a * kStageA + kk * 16 * BM, BM);
+      else fa[dst][i] = *(const i32x4*)(base + slot_a * kStageA + (wm * TM + i) * 4096);
     }
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
-      if constexpr (B_ACROSS) fb[dst][j] = read_across(b_at[j] + slot * kStage + kk * 16 * BN, BN);
-      else fb[dst][j] = *(const i32x4*)(base + BM * 128 + (wn * TN + j) * 4096);
+      if constexpr (B_ACROSS) fb[dst][j] = read_across(b_at[j] + slot_b * kStageB + kk * 16 * BN, BN);
+      else fb[dst][j] = *(const i32x4*)(base + kRingB + slot_b * kStageB + (wn * TN + j) * 4096);
     }
   };
   constexpr int kMfma = TM * TN, kSplit = kMfma > 1 ? kMfma / 2 : 1;
@@ -288,19 +305,23 @@ __global__ __launch_bounds__(256) void ffn_tile(TileArgs p) {
 
   if (s_begin < s_end) {
 #pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s) {
-      enter_stage(s_begin + s);
+    for (int i = 1 - SB; i < 0; ++i) {   // as the stages before the first would have
+      enter_stage(s_begin + i + SA - 1, s_begin + i + SB - 1);
 #pragma unroll
-      for (int t = 0; t < kSlots; ++t) issue_load(t, s_begin + s, s);
+      for (int t = 0; t < kSlots; ++t) {
+        if (t >= kSlotsA) issue_load(t, s_begin + i + SB - 1, i + SB - 1);
+        else if (i + SA - 1 >= 0) issue_load(t, s_begin + i + SA - 1, i + SA - 1);
+      }
     }
     wait_vmcnt<kInFlight>();
     block_barrier();
-    read_frags(0, 0, 0);
-    int slot = 0;
+    read_frags(0, 0, 0, 0);
+    int slot_a = 0, slot_b = 0;
     for (int s = s_begin; s < s_end; ++s) {
-      const int sl = s + STAGES - 1;   // (past the last stage the loads move no data)
-      const int slot_l = slot == 0 ? STAGES - 1 : slot - 1, slot_n = slot == STAGES - 1 ? 0 : slot + 1;
-      enter_stage(sl);
+      // (past the last stage the loads move no data)
+      const int load_a = slot_a == 0 ? SA - 1 : slot_a - 1, next_a = slot_a == SA - 1 ? 0 : slot_a + 1;
+      const int load_b = slot_b == 0 ? SB - 1 : slot_b - 1, next_b = slot_b == SB - 1 ? 0 : slot_b + 1;
+      enter_stage(s + SA - 1, s + SB - 1);
       auto step = [&](auto kk_c) __attribute__((always_inline)) {
         constexpr int kk = decltype(kk_c)::value;
         constexpr int src = kk & 1, dst = src ^ 1;
@@ -314,12 +335,12 @@ __global__ __launch_bounds__(256) void ffn_tile(TileArgs p) {
               ++pre;
               __builtin_amdgcn_sched_barrier(0);
             }
-            issue_load(t, sl, slot_l);
+            issue_load(t, t < kSlotsA ? s + SA - 1 : s + SB - 1, t < kSlotsA ? load_a : load_b);
             __builtin_amdgcn_sched_barrier(0);
           }
         }
         if constexpr (kk < 3) {
-          read_frags(slot, kk + 1, dst);
+          read_frags(slot_a, slot_b, kk + 1, dst);
           compute(src, pre, kMfma);
           interleave(kMfma - pre, kReads);
         } else {
@@ -329,7 +350,7 @@ __global__ __launch_bounds__(256) void ffn_tile(TileArgs p) {
           wait_vmcnt<kInFlight>();   // own loads of stage s + 1 landed
           wait_lgkmcnt0();           // own reads of stage s done
           block_barrier();           // ... everyone's
-          read_frags(slot_n, 0, dst);
+          read_frags(next_a, next_b, 0, dst);
           compute(src, kSplit, kMfma);
           interleave(kMfma - kSplit, kReads);
         }
@@ -338,7 +359,8 @@ __global__ __launch_bounds__(256) void ffn_tile(TileArgs p) {
       step(std::integral_constant<int, 1>());
       step(std::integral_constant<int, 2>());
       step(std::integral_constant<int, 3>());
-      slot = slot_n;
+      slot_a = next_a;
+      slot_b = next_b;
     }
   }
 
@@ -380,11 +402,11 @@ __global__ __launch_bounds__(256) void ffn_tile(TileArgs p) {
       if constexpr (GATED) staged(r, c + WTN / 2, u);
       if (row < p.M && col < columns) {
         if (p.splits > 1) {
-          f32x4* part = (f32x4*)(p.part + ((size_t)blockIdx.y * p.M + row) * p.N + col);
+          f32x4* part = (f32x4*)(p.part + ((size_t)blockIdx.y * p.M + row) * p.part_stride + col);
           part[0] = f32x4{v[0], v[1], v[2], v[3]};
           part[1] = f32x4{v[4], v[5], v[6], v[7]};
           if constexpr (GATED) {
-            part = (f32x4*)((float*)part + p.F);
+            part = (f32x4*)((float*)part + p.part_stride / 2);
             part[0] = f32x4{u[0], u[1], u[2], u[3]};
             part[1] = f32x4{u[4], u[5], u[6], u[7]};
           }

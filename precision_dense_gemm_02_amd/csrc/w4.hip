@@ -2,6 +2,13 @@
 // (include/lpgemm_ffn.h).
 #include "few_rows.hpp"
 #include "w4_kernels.hpp"
+#include "ffn.hpp"
+#include "w4_tile.hpp"
+
+namespace lpgemm {
+int g_w4_bm = -1, g_w4_splits = 0;
+}
+extern "C" void lpgemm_tune_w4(int bm, int splits) { lpgemm::g_w4_bm = bm; lpgemm::g_w4_splits = splits; }
 
 using namespace lpgemm;
 
@@ -40,6 +47,37 @@ const void* dequantize_kernel(lpgemm_type out) {
                              : (const void*)&dequantize_w4_kernel<T, 2>;
 }
 
+// The workspace of a plan, in bytes from its start: W4_WHOLE the weights in 16
+// bits and the splits' sums, W4_TILE the splits' sums.
+struct W4Space {
+  int64_t part, total;
+  W4Space(const W4Plan& plan, int64_t M, int64_t N, int64_t F, int64_t K, int cu_count) {
+    part = plan.way == W4_WHOLE ? (2 * N * K + 255) / 256 * 256 : 0;
+    const int job = F > 0 ? JOB_GATED : JOB_DOWN;
+    total = part + (plan.way == W4_WHOLE ? split_bytes(plan_tiles(job, M, N, K, cu_count), job, M, N) : w4_part_bytes(plan, M, N));
+  }
+};
+
+template <typename T>
+lpgemm_status run_whole(int64_t group, const W4TileArgs& w, uint8_t* ws, float* part, int cu_count, hipStream_t stream) {
+  const lpgemm_type type = kIsF16<T> ? LPGEMM_F16 : LPGEMM_BF16;
+  lpgemm_status st = lpgemm_dequantize_w4(w.N, w.K, group, type, w.W, w.scales, w.zeros, type, ws, stream);
+  if (st != LPGEMM_SUCCESS) return st;
+  TileArgs p{};
+  p.A = w.X;
+  p.B = ws;
+  p.a_stride = w.x_stride;
+  p.b_stride = 2 * (int64_t)w.K;
+  p.C = p.H = w.C;
+  p.out_type = w.out_type;
+  p.activation = w.activation;
+  p.M = w.M;
+  p.N = w.N;
+  p.F = w.F;
+  p.K = w.K;
+  return run_tile<T>(w.F > 0 ? JOB_GATED : JOB_DOWN, p, part, cu_count, stream);
+}
+
 // The product, and (F > 0) the gated product.
 lpgemm_status product(int64_t M, int64_t N, int64_t F, int64_t K, int64_t group, lpgemm_type type, int activation,
                       const void* X, int64_t x_stride, const uint8_t* codes, const void* scales, const void* zeros,
@@ -54,7 +92,32 @@ lpgemm_status product(int64_t M, int64_t N, int64_t F, int64_t K, int64_t group,
   DeviceInfo dev;
   const lpgemm_status st = current_device(dev);
   if (st != LPGEMM_SUCCESS) return st;
-  FewRowsArgs p{};
+  const W4Plan plan = plan_w4(M, N, K, dev.cu_count);
+  const W4Space space(plan, M, N, F, K, dev.cu_count);
+  const int64_t need = space.total;
+  if (need > 0 && (!workspace || workspace_bytes < need)) return LPGEMM_ERROR_INVALID_VALUE;
+  const int w4 = group == 32 ? 1 : group == 64 ? 2 : 4;
+  if (plan.way == W4_FEW_ROWS) {
+    FewRowsArgs p{};
+    p.X = static_cast<const uint8_t*>(X);
+    p.W = codes;
+    p.scales = static_cast<const uint16_t*>(scales);
+    p.zeros = static_cast<const uint16_t*>(zeros);
+    p.C = static_cast<uint8_t*>(C);
+    p.out_type = out_type;
+    p.M = (int)M;
+    p.N = (int)N;
+    p.F = (int)F;
+    p.K = (int)K;
+    p.activation = activation;
+    p.x_stride = (int)(2 * x_stride);
+    p.row_bytes = (int)(K / 2);
+    p.groups = (int)(K / group);
+    p.group_shift = group == 256 ? 1 : 0;
+    return type == LPGEMM_F16 ? run_few_rows<TypeF16>(p, w4, dev.cu_count, stream)
+                              : run_few_rows<TypeBF16>(p, w4, dev.cu_count, stream);
+  }
+  W4TileArgs p{};
   p.X = static_cast<const uint8_t*>(X);
   p.W = codes;
   p.scales = static_cast<const uint16_t*>(scales);
@@ -69,10 +132,19 @@ lpgemm_status product(int64_t M, int64_t N, int64_t F, int64_t K, int64_t group,
   p.x_stride = (int)(2 * x_stride);
   p.row_bytes = (int)(K / 2);
   p.groups = (int)(K / group);
-  p.group_shift = group == 256 ? 1 : 0;
-  const int w4 = group == 32 ? 1 : group == 64 ? 2 : 4;
-  return type == LPGEMM_F16 ? run_few_rows<TypeF16>(p, w4, dev.cu_count, stream)
-                            : run_few_rows<TypeBF16>(p, w4, dev.cu_count, stream);
+  p.group_shift = log2_of(group);
+  uint8_t* const ws = static_cast<uint8_t*>(workspace);
+  p.part = reinterpret_cast<float*>(ws + space.part);
+  if (plan.way == W4_WHOLE)
+    return type == LPGEMM_F16 ? run_whole<TypeF16>(group, p, ws, p.part, dev.cu_count, stream)
+                              : run_whole<TypeBF16>(group, p, ws, p.part, dev.cu_count, stream);
+  if (type == LPGEMM_F16)
+    return w4 == 1   ? run_w4_tile<TypeF16, 1>(plan, p, stream)
+           : w4 == 2 ? run_w4_tile<TypeF16, 2>(plan, p, stream)
+                     : run_w4_tile<TypeF16, 4>(plan, p, stream);
+  return w4 == 1   ? run_w4_tile<TypeBF16, 1>(plan, p, stream)
+         : w4 == 2 ? run_w4_tile<TypeBF16, 2>(plan, p, stream)
+                   : run_w4_tile<TypeBF16, 4>(plan, p, stream);
 }
 
 }  // namespace
@@ -137,9 +209,13 @@ lpgemm_status lpgemm_dequantize_w4(int64_t N, int64_t K, int64_t group, lpgemm_t
   return st;
 }
 
-int64_t lpgemm_w4_workspace(int64_t M, int64_t K, int64_t group) {
-  if (M < 0 || K < 0 || M > INT32_MAX || bad_group(K, group)) return -1;
-  return 0;
+int64_t lpgemm_w4_workspace(int64_t M, int64_t N, int64_t K, int64_t group, int gated) {
+  if (M < 0 || N < 0 || K < 0 || M > INT32_MAX || N > INT32_MAX || bad_group(K, group) || (gated && N % 2 != 0)) return -1;
+  if (M == 0 || N == 0) return 0;
+  DeviceInfo dev;
+  if (current_device(dev) != LPGEMM_SUCCESS) return -1;
+  const W4Plan plan = plan_w4(M, N, K, dev.cu_count);
+  return W4Space(plan, M, N, gated ? N / 2 : 0, K, dev.cu_count).total;
 }
 
 lpgemm_status lpgemm_w4(int64_t M, int64_t N, int64_t K, int64_t group, lpgemm_type type, const void* X,

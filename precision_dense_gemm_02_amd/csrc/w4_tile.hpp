@@ -1,0 +1,79 @@
+// Host side of the products with 4-bit weights: the kernel for the sizes and
+// its launch.  run_w4_tile<T, STEPS> is instantiated in translation units of
+// its own (run_w4_*.hip).
+#pragma once
+
+#include "../../include/lpgemm_ffn.h"
+#include "dispatch.hpp"
+#include "w4_tile_kernels.hpp"
+
+namespace lpgemm {
+
+enum W4Way {
+  W4_FEW_ROWS = 0,   // few_rows
+  W4_TILE = 1,       // w4_tile
+  W4_WHOLE = 2,      // the weights as 16-bit values in the workspace, then the block's tiles
+};
+struct W4Plan {
+  int way;
+  int bm;            // W4_TILE: 32 or 64 rows by 128 columns
+  int splits;
+};
+
+extern int g_w4_bm, g_w4_splits;
+
+// Up to this many rows the weights enter the sums exactly; beyond, they are
+// first written out as 16-bit values, each rounded once.
+constexpr int kW4ExactRows = LPGEMM_W4_EXACT_M;
+
+// N: weight rows (gated: both projections').
+inline W4Plan plan_w4(int64_t M, int64_t N, int64_t K, int cu_count) {
+  const int64_t weights = N * K;
+  W4Plan plan{W4_TILE, 32, 1};
+  if (M > kW4ExactRows) plan.way = W4_WHOLE;
+  else if (M <= LPGEMM_W4_SHORT_M || (M <= 16 && N < 20480) || weights <= (M <= 32 ? (int64_t)20 << 20 : M <= 64 ? (int64_t)8 << 20 : 0))
+    plan.way = W4_FEW_ROWS;
+  if (g_w4_bm >= 0) plan.way = g_w4_bm == 0 ? W4_FEW_ROWS : g_w4_bm == 1 ? W4_WHOLE : W4_TILE;
+  if (plan.way != W4_TILE) return plan;
+  if ((int64_t)tiles(M, 32) * tiles(N, 128) > cu_count) plan.bm = 64;
+  if (g_w4_bm >= 32) plan.bm = g_w4_bm;
+  const int64_t n = (int64_t)tiles(M, plan.bm) * tiles(N, 128), stages = tiles(K, 128);
+  int64_t s = cu_count / n;
+  if (s > stages / 8) s = stages / 8;
+  if (s > 16) s = 16;
+  if (s > 1) plan.splits = (int)s;
+  if (g_w4_splits > 0) plan.splits = (int)(g_w4_splits < stages ? g_w4_splits : stages);
+  return plan;
+}
+
+inline int64_t w4_part_bytes(const W4Plan& p, int64_t M, int64_t N) { return p.way == W4_TILE && p.splits > 1 ? 4 * p.splits * M * N : 0; }
+
+template <typename T, int STEPS>
+lpgemm_status run_w4_tile(const W4Plan& plan, W4TileArgs p, hipStream_t stream);
+
+#ifdef LPGEMM_W4_DEFINE
+template <typename T, int STEPS, bool GATED>
+const void* w4_kernel(int bm) {
+  return bm == 32 ? (const void*)&w4_tile<T, STEPS, 32, 2, 4, GATED> : (const void*)&w4_tile<T, STEPS, 64, 2, 2, GATED>;
+}
+
+template <typename T, int STEPS>
+lpgemm_status run_w4_tile(const W4Plan& plan, W4TileArgs p, hipStream_t stream) {
+  p.stages = tiles(p.K, 128);
+  p.split_stages = tiles(p.stages, plan.splits);
+  p.splits = plan.splits;
+  p.tiles_m = tiles(p.M, plan.bm);
+  p.tiles_n = p.F > 0 ? tiles(p.F, 64) : tiles(p.N, 128);
+  void* kargs[] = {&p};
+  const void* fn = p.F > 0 ? w4_kernel<T, STEPS, true>(plan.bm) : w4_kernel<T, STEPS, false>(plan.bm);
+  if (hipLaunchKernel(fn, dim3((unsigned)(p.tiles_m * p.tiles_n), (unsigned)plan.splits), dim3(plan.bm == 32 ? 1024 : 512), kargs, 0, stream) != hipSuccess)
+    return LPGEMM_ERROR_LAUNCH;
+  if (plan.splits == 1) return LPGEMM_SUCCESS;
+  const int64_t n = (int64_t)p.M * (p.F > 0 ? p.F : p.N);
+  return hipLaunchKernel((const void*)&join_w4<T>, dim3((unsigned)((n + 255) / 256)), dim3(256), kargs, 0, stream) == hipSuccess
+             ? LPGEMM_SUCCESS
+             : LPGEMM_ERROR_LAUNCH;
+}
+#endif
+
+}  // namespace lpgemm
