@@ -34,18 +34,24 @@ __device__ __forceinline__ float activate(float g, int kind) {
   return g * logistic(kind == kSilu ? g : gelu_argument(g));
 }
 
-// act(g) and act'(g).  With p = logistic(a(g)): act = g p, act' = p + g a' p (1
-// - p), and 1 - p = logistic(-a), which does not cancel.  Past |g| = 16 the
-// second term of GELU's derivative is below 2^-140; clamped there, g^2 a' stays
-// finite for every g.
+// act(g) and act'(g), for results that are rounded to 16 bits.  With p =
+// logistic(a(g)): act = g p, act' = p + g a' p (1 - p).  p and 1 - p are 1 / (1 +
+// e) and e / (1 + e) with e = exp(-|a|), which neither cancels nor overflows.
+// The exponential is one instruction, off by |a| units of 2^-24: at most 2^-17
+// of the value.  Past |g| = 16 the second term of GELU's derivative is below
+// 2^-140; clamped there, g^2 a' stays finite.
 __device__ __forceinline__ void activate_with_slope(float g, int kind, float& act, float& slope) {
   const float a = kind == kSilu ? g : gelu_argument(g);
-  const float p = logistic(a), rest = logistic(-a);
+  const float e = __builtin_amdgcn_exp2f(-1.442695041f * __builtin_fabsf(a));
+  const float more = __builtin_amdgcn_rcpf(1.f + e), less = e * more;
+  const float p = a < 0.f ? less : more, rest = a < 0.f ? more : less;
   act = g * p;
-  const float gc = kind == kSilu ? g : __builtin_amdgcn_fmed3f(g, -16.f, 16.f);
-  const float da = kind == kSilu ? 1.f : __builtin_fmaf(3.f * kGelu3, gc * gc, kGelu1);
-  // (p is a number also where g is not)
-  slope = __builtin_fmaf(gc * da * rest, p, p) + (g - g);
+  if (kind == kSilu) {
+    slope = __builtin_fmaf(act, rest, p);
+  } else {
+    const float gc = __builtin_amdgcn_fmed3f(g, -16.f, 16.f);
+    slope = __builtin_fmaf(gc * __builtin_fmaf(3.f * kGelu3, gc * gc, kGelu1) * rest, p, p);
+  }
 }
 
 }  // namespace lpgemm

@@ -65,7 +65,7 @@ lpgemm_status run_few_rows(const FewRowsArgs& args, int w4, int cu_count, hipStr
     else waves = gated ? 8 : 16;
   } else {
     if (many) nb = 2, waves = 4;
-    else if (tiles(p.M, 32) > 1) nb = 2;
+    else if (w4 && tiles(p.M, 32) > 1) nb = 2;
   }
   if (g_few_rows_nb > 0 && !(gated && g_few_rows_nb == 1) && !(mt > 1 && g_few_rows_nb == 4)) nb = g_few_rows_nb;
   if (g_few_rows_waves > 0) waves = g_few_rows_waves;

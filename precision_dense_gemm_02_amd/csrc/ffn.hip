@@ -3,11 +3,8 @@
 #include "few_rows.hpp"
 
 namespace lpgemm {
-int g_tile_bm[5], g_tile_splits[5], g_few_limit = 64;
 int g_few_rows_nb = 0, g_few_rows_waves = 0, g_few_rows_lds = 64;
 }
-extern "C" void lpgemm_tune_tile(int job, int bm, int splits) { lpgemm::g_tile_bm[job] = bm; lpgemm::g_tile_splits[job] = splits; }
-extern "C" void lpgemm_tune_limit(int m) { lpgemm::g_few_limit = m; }
 extern "C" void lpgemm_tune_few_rows(int nb, int waves, int lds) { lpgemm::g_few_rows_nb = nb; lpgemm::g_few_rows_waves = waves; lpgemm::g_few_rows_lds = lds; }
 
 using namespace lpgemm;
@@ -26,8 +23,11 @@ bool bad_shape(int64_t M, int64_t D, int64_t F) {
 }
 bool bad_stride(int64_t stride, int64_t D) { return stride < D || stride % 8 != 0 || stride > LPGEMM_MAX_STRIDE; }
 
-// Up to this many rows the forward pass runs its products of few rows.
-constexpr int kFewRows = 64;
+// Whether the forward pass runs its products on few_rows: a handful of rows, or
+// small weights (us, both products, few_rows against tiles: 8 x 4096 x 14336 75
+// and 77, 16 rows 85 and 78; 33 x 1024 x 2816 16.2 and 19.6, 64 rows 21.0 and
+// 20.2).
+bool few_rows_forward(int64_t M, int64_t D, int64_t F) { return M <= 8 || (M <= 48 && D * F <= (int64_t)4 << 20); }
 
 // The workspace's parts, in bytes from its start.
 struct ForwardSpace {
@@ -36,7 +36,7 @@ struct ForwardSpace {
     h = 0;
     part = round256(2 * M * F);
     int64_t sums = 0;
-    if (M > g_few_limit) {
+    if (!few_rows_forward(M, D, F)) {
       const int64_t a = split_bytes(plan_tiles(JOB_GATED, M, 2 * F, D, cu_count), JOB_GATED, M, 2 * F);
       const int64_t b = split_bytes(plan_tiles(JOB_DOWN, M, D, F, cu_count), JOB_DOWN, M, D);
       sums = a > b ? a : b;
@@ -78,7 +78,7 @@ lpgemm_status forward(int64_t M, int64_t D, int64_t F, int activation, const voi
   const ForwardSpace space(M, D, F, cu_count);
   uint8_t* const h = ws + space.h;
   lpgemm_status st = LPGEMM_SUCCESS;
-  if (M <= g_few_limit) {
+  if (few_rows_forward(M, D, F)) {
     FewRowsArgs p{};
     p.X = static_cast<const uint8_t*>(X);
     p.W = static_cast<const uint8_t*>(w_gate_up);

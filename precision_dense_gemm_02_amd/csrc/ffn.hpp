@@ -23,24 +23,43 @@ struct TilePlan {
   int splits;
 };
 
-extern int g_tile_bm[5], g_tile_splits[5], g_few_limit;
-
-// The tile and the splits of an M x N product over K (gated: N = 2 F).
+// The tile and the splits of an M x N product over K (gated: N = 2 F): of the
+// kernels' three tiles and up to 16 splits the pair whose time a model puts
+// lowest.  The model, in us: the workgroups fill the CUs in rounds (two on a CU
+// with tiles of 64 and 128 rows, one with 256); a round takes its stages, each
+// longer the more workgroups share the chip, and a fixed time for its first
+// loads and its end (which is longer where the end has an activation); splits
+// add a launch and the traffic of their sums.  Its numbers were fitted to the
+// times of every pair at 130 products (M, N and K of blocks of 16 to 4096 rows,
+// D = 1024 to 4096, F = 1416 to 14336, one MI355X).  At these the choice is 1.2%
+// of the product's time behind the best pair on average, 21% at the worst.
 inline TilePlan plan_tiles(int job, int64_t M, int64_t N, int64_t K, int cu_count) {
-  auto count = [&](int bm, int bn) { return (int64_t)tiles(M, bm) * tiles(N, bn); };
-  TilePlan plan{64, 128, 1};
-  if (2 * count(256, 256) > cu_count && M > 128) plan = {256, 256, 1};
-  else if (2 * count(128, 128) > cu_count && M > 64) plan = {128, 128, 1};
-  if (g_tile_bm[job]) plan = {g_tile_bm[job], g_tile_bm[job] == 64 ? 128 : g_tile_bm[job], 1};
-  const int64_t stages = tiles(K, 64), n = count(plan.bm, plan.bn);
-  if (n > 0 && n * 2 <= cu_count) {
-    int64_t s = cu_count / n;
-    if (s > stages / 4) s = stages / 4;
-    if (s > 16) s = 16;
-    if (s > 1) plan.splits = (int)s;
+  struct Tile {
+    int bm, bn, per_cu;
+    double stage, stage_full, ends;   // a stage with few workgroups and with all places taken, a workgroup's start and end
+  };
+  constexpr Tile kTiles[] = {{64, 128, 2, 0.433, 0.96, 4.19}, {128, 128, 2, 0.527, 1.045, 7.51}, {256, 256, 1, 1.033, 1.33, 20.8}};
+  const double end_factor = job == JOB_GATED_GRAD ? 1.71 : job == JOB_GATED ? 1.43 : 1.0;
+  const double stages = (double)((K + 63) / 64);
+  TilePlan best{64, 128, 1};
+  double least = 1e300;
+  for (const Tile& t : kTiles) {
+    const double count = (double)((M + t.bm - 1) / t.bm) * (double)((N + t.bn - 1) / t.bn), places = (double)cu_count * t.per_cu;
+    for (int splits = 1; splits <= 16 && (splits == 1 || 2 * splits <= stages); splits *= 2) {
+      const double per_split = (double)(((int64_t)stages + splits - 1) / splits);
+      auto round = [&](double workgroups) {
+        const double shared = t.per_cu == 2 ? (workgroups - cu_count) / cu_count : (workgroups - cu_count / 4) / (0.75 * cu_count);
+        const double share = shared < 0 ? 0 : shared > 1 ? 1 : shared;
+        return workgroups > 0 ? per_split * (t.stage + (t.stage_full - t.stage) * share) + end_factor * t.ends : 0.0;
+      };
+      const double all = count * splits, full = (double)(int64_t)(all / places);
+      // (many rounds: the workgroups no longer move together)
+      double time = all > 4 * places ? (all / places + 0.3) * round(places) : full * round(places) + round(all - full * places);
+      if (splits > 1) time += 6.19 + 0.355 * splits + (double)M * (double)N * (8.0 * splits + (job == JOB_GATED_GRAD ? 10 : 2)) / 10.0e6;
+      if (time < least) least = time, best = {t.bm, t.bn, splits};
+    }
   }
-  if (g_tile_splits[job]) plan.splits = (int)(g_tile_splits[job] < stages ? g_tile_splits[job] : stages ? stages : 1);
-  return plan;
+  return best;
 }
 
 // A row of a split's sums: chunks of eight columns (gated: both projections').

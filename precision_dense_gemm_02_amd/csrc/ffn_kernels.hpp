@@ -68,6 +68,25 @@ __device__ __forceinline__ void store_columns(uint8_t* C, int out_type, int row,
   }
 }
 
+// The gradients of eight gates and up values, and h again.
+template <typename T>
+__device__ __forceinline__ void finish8_grad(const TileArgs& p, int row, int col, const float (&dh)[8], const i32x4& gate, const i32x4& up) {
+  const f32x8 g = widen<T>(gate), u = widen<T>(up);
+  float dg[8], du[8], h[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    float act, slope;
+    activate_with_slope(g[e], p.activation, act, slope);
+    dg[e] = dh[e] * u[e] * slope;
+    du[e] = dh[e] * act;
+    h[e] = act * u[e];
+  }
+  uint8_t* const dgu = p.DGU + 2 * ((size_t)row * 2 * p.F + col);
+  *(i32x4*)dgu = narrow8<T>(dg);
+  *(i32x4*)(dgu + 2 * (size_t)p.F) = narrow8<T>(du);
+  *(i32x4*)(p.H + 2 * ((size_t)row * p.F + col)) = narrow8<T>(h);
+}
+
 // Eight consecutive columns of one row: what END does with them.  `v`: the sums
 // (END_GATED: of the gate), `u`: those of the up projection.
 template <typename T, int END>
@@ -85,20 +104,8 @@ __device__ __forceinline__ void finish8(const TileArgs& p, int row, int col, con
     }
     store_columns(p.H, p.out_type, row, col, p.F, h);
   } else {
-    const size_t at = 2 * ((size_t)row * 2 * p.F + col);
-    const f32x8 g = widen<T>(*(const i32x4*)(p.GU + at)), up = widen<T>(*(const i32x4*)(p.GU + at + 2 * (size_t)p.F));
-    float dg[8], du[8], h[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float act, slope;
-      activate_with_slope(g[e], p.activation, act, slope);
-      dg[e] = v[e] * up[e] * slope;
-      du[e] = v[e] * act;
-      h[e] = act * up[e];
-    }
-    *(i32x4*)(p.DGU + at) = narrow8<T>(dg);
-    *(i32x4*)(p.DGU + at + 2 * (size_t)p.F) = narrow8<T>(du);
-    *(i32x4*)(p.H + 2 * ((size_t)row * p.F + col)) = narrow8<T>(h);
+    const uint8_t* gu = p.GU + 2 * ((size_t)row * 2 * p.F + col);
+    finish8_grad<T>(p, row, col, v, *(const i32x4*)gu, *(const i32x4*)(gu + 2 * (size_t)p.F));
   }
 }
 
@@ -151,11 +158,7 @@ __global__ __launch_bounds__(256) void ffn_tile(TileArgs p) {
   constexpr bool GATED = END == END_GATED;
   constexpr int kStageA = BM * 128, kStageB = BN * 128, kRingB = SA * kStageA;
   constexpr int kSlots = (BM + BN) / 32, kSlotsA = BM / 32, kSlotsB = BN / 32;   // 1 KiB loads per wave and stage
-  constexpr int kEpiPitch = WTN * 4 + 32;
-  constexpr int kEpiRows = WTM < 64 ? WTM : 64;
-  constexpr int kEpiWave = kEpiRows * kEpiPitch;
-  constexpr int kRings = kRingB + SB * kStageB;
-  constexpr int kLds = kRings > 4 * kEpiWave ? kRings : 4 * kEpiWave;
+  constexpr int kLds = kRingB + SB * kStageB;
   static_assert(kLds <= 160 * 1024, "LDS");
   // loads that may be in flight once stage s + 1 has landed: those behind the
   // later of A's and B's, which go out in stages s + 2 - SA and s + 2 - SB, A's
@@ -284,13 +287,13 @@ __global__ __launch_bounds__(256) void ffn_tile(TileArgs p) {
       else fb[dst][j] = *(const i32x4*)(base + kRingB + slot_b * kStageB + (wn * TN + j) * 4096);
     }
   };
-  constexpr int kMfma = TM * TN, kSplit = kMfma > 1 ? kMfma / 2 : 1;
+  constexpr int kMfma = TM * TN, kSplit = kMfma > 8 ? 3 : kMfma > 1 ? kMfma / 2 : 1;
   constexpr int kReads = TM * (A_ACROSS ? 2 : 1) + TN * (B_ACROSS ? 2 : 1);
   auto compute = [&](int src, int first, int last) __attribute__((always_inline)) {
 #pragma unroll
     for (int x = 0; x < kMfma; ++x) {
       if (x < first || x >= last) continue;
-      acc[x / TN][x % TN] = mfma32<T>(fa[src][x / TN], fb[src][x % TN], acc[x / TN][x % TN]);
+      acc[x / TN][x % TN] = mfma32<T>(fb[src][x % TN], fa[src][x / TN], acc[x / TN][x % TN]);
     }
   };
   auto interleave = [&](int mfmas, int reads) __attribute__((always_inline)) {
@@ -364,58 +367,62 @@ __global__ __launch_bounds__(256) void ffn_tile(TileArgs p) {
     }
   }
 
-  // Every outstanding load (all past the last stage) lands before LDS is
-  // reused, and every wave is done reading; then each wave turns kEpiRows rows
-  // of its part at a time through LDS, so that a lane holds 8 consecutive
-  // columns of one row.
-  wait_vmcnt<0>();
-  wait_lgkmcnt0();
-  block_barrier();
-  uint8_t* const stage_out = smem + wave * kEpiWave;
-  constexpr int kWaveColumns = GATED ? WTN / 2 : WTN;
-  constexpr int kLanesPerRow = kWaveColumns / 8, kRowsPerStore = 64 / kLanesPerRow;
-  const int c = (lane % kLanesPerRow) * 8, col = n0 + wn * kWaveColumns + c;
+  wait_vmcnt<0>();   // (loads past the last stage: LDS is the next workgroup's once this one ends)
+  // The matrix instructions have B's rows as theirs: a lane holds one row of C,
+  // and of its columns four at a time, 8 q + 4 (l / 32) .. + 3 of each 32.  Two
+  // such runs, exchanged between the half-waves, are eight consecutive columns.
+  constexpr int kBlocks = GATED ? TN / 2 : TN;   // column blocks of C
+  const int wave_col = n0 + wn * (GATED ? WTN / 2 : WTN) + 8 * fh;
+  auto eight = [&](const f32x16& x, int q, float (&v)[8]) __attribute__((always_inline)) {
 #pragma unroll
-  for (int pass = 0; pass < WTM / kEpiRows; ++pass) {
+    for (int e = 0; e < 4; ++e) {
+      const float lo = x[8 * q + e], hi = x[8 * q + 4 + e];
+      const u32x2 t = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi), false, false));
+      const uint32_t first = t.x, second = t.y;
+      v[e] = __builtin_bit_cast(float, first);
+      v[4 + e] = __builtin_bit_cast(float, second);
+    }
+  };
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
+  for (int i = 0; i < TM; ++i) {
+    const int row = m0 + wm * WTM + 32 * i + fr;
+    __builtin_amdgcn_sched_barrier(0);   // (else the compiler reads every accumulator out at once)
 #pragma unroll
-      for (int j = 0; j < TN; ++j)
+    for (int j = 0; j < TN; ++j) asm volatile("" : "+a"(acc[i][j]));
+    i32x4 kept[END == END_GATED_GRAD ? 4 * kBlocks : 1];   // g and u of the block's chunks, loaded together
+    if constexpr (END == END_GATED_GRAD) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int rg = i * 32 + 8 * (e >> 2);
-          if (rg / kEpiRows != pass) continue;
-          *(float*)(stage_out + (rg - pass * kEpiRows + 4 * fh + (e & 3)) * kEpiPitch + (j * 32 + fr) * 4) = acc[i][j][e];
-        }
-    wait_lgkmcnt0();   // this wave's LDS writes done
-    auto staged = [&](int r, int at, float (&v)[8]) {
-      const f32x4 a = *(const f32x4*)(stage_out + r * kEpiPitch + at * 4), b = *(const f32x4*)(stage_out + r * kEpiPitch + at * 4 + 16);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = a[e], v[4 + e] = b[e];
-    };
-#pragma unroll
-    for (int r0 = 0; r0 < kEpiRows; r0 += kRowsPerStore) {
-      const int r = r0 + lane / kLanesPerRow;
-      const int row = m0 + wm * WTM + pass * kEpiRows + r;
-      float v[8], u[8] = {};
-      staged(r, c, v);
-      if constexpr (GATED) staged(r, c + WTN / 2, u);
-      if (row < p.M && col < columns) {
-        if (p.splits > 1) {
-          f32x4* part = (f32x4*)(p.part + ((size_t)blockIdx.y * p.M + row) * p.part_stride + col);
-          part[0] = f32x4{v[0], v[1], v[2], v[3]};
-          part[1] = f32x4{v[4], v[5], v[6], v[7]};
-          if constexpr (GATED) {
-            part = (f32x4*)((float*)part + p.part_stride / 2);
-            part[0] = f32x4{u[0], u[1], u[2], u[3]};
-            part[1] = f32x4{u[4], u[5], u[6], u[7]};
-          }
-        } else {
-          finish8<T, END>(p, row, col, v, u);
+      for (int c = 0; c < 2 * kBlocks; ++c) {
+        const int col = wave_col + 16 * c;
+        if (p.splits == 1 && row < p.M && col < columns) {
+          const uint8_t* gu = p.GU + 2 * ((size_t)row * 2 * p.F + col);
+          kept[2 * c] = *(const i32x4*)gu;
+          kept[2 * c + 1] = *(const i32x4*)(gu + 2 * (size_t)p.F);
         }
       }
     }
-    wait_lgkmcnt0();   // reads done before the next pass overwrites them
+#pragma unroll
+    for (int c = 0; c < 2 * kBlocks; ++c) {
+      const int col = wave_col + 16 * c;
+      float v[8], u[8] = {};
+      eight(acc[i][c / 2], c % 2, v);
+      if constexpr (GATED) eight(acc[i][c / 2 + kBlocks], c % 2, u);
+      if (row >= p.M || col >= columns) continue;
+      if (p.splits > 1) {
+        f32x4* part = (f32x4*)(p.part + ((size_t)blockIdx.y * p.M + row) * p.part_stride + col);
+        part[0] = f32x4{v[0], v[1], v[2], v[3]};
+        part[1] = f32x4{v[4], v[5], v[6], v[7]};
+        if constexpr (GATED) {
+          part = (f32x4*)((float*)part + p.part_stride / 2);
+          part[0] = f32x4{u[0], u[1], u[2], u[3]};
+          part[1] = f32x4{u[4], u[5], u[6], u[7]};
+        }
+      } else if constexpr (END == END_GATED_GRAD) {
+        finish8_grad<T>(p, row, col, v, kept[2 * c], kept[2 * c + 1]);
+      } else {
+        finish8<T, END>(p, row, col, v, u);
+      }
+    }
   }
 }
 
