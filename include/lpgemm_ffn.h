@@ -13,7 +13,7 @@
  * the caller, work enqueued on `stream` without synchronising, nothing
  * allocated, no state kept between calls, the same status codes checked on the
  * host in the same order (sizes, shape rules, empty problem, NULL pointers,
- * alignment, workspace, then the device and the launch).  Weights are N rows
+ * alignment, then the device, the workspace's size and the launch).  Weights are N rows
  * of K values.  Outputs must not overlap inputs, each other or the workspace.
  *
  * Sixteen-bit tensors are binary16 or bfloat16; `type` is the type of every
@@ -78,18 +78,23 @@ lpgemm_status lpgemm_dequantize_w4(int64_t N, int64_t K, int64_t group, lpgemm_t
 
 /* C = X . W^T: X M rows of K values of `type` (x_stride in elements, at least
  * K, a multiple of 8, at most LPGEMM_MAX_STRIDE), W in 4 bits with scales and
- * zeros of the same type, C M x N of `out_type`.  The weights enter the sums
- * exactly: C[m][n] = sum over groups of scale * (sum of x * code - zero * sum
- * of x), every sum in binary32.  A row of X with an infinity or a NaN gives NaN
- * (the kernels sum x * (code + 24) and take 24 times the sum of x off), and so
- * may one with magnitudes above 2^115.  M = 0 or N = 0 is a no-op; K = 0 sets C
- * to 0.
- * X, codes and C 16-byte aligned, scales and zeros 2-byte.  M and N at most
- * 2^31 - 257 and below 2^24 tiles of C (UNSUPPORTED_SHAPE otherwise).
- * `workspace`, 16-byte aligned, holds at least lpgemm_w4_workspace(M, K, group)
- * bytes (0 up to LPGEMM_W4_SHORT_M rows; -1 for sizes out of range);
+ * zeros of the same type, C M x N of `out_type`.  Up to LPGEMM_W4_EXACT_M rows
+ * the weights enter the sums exactly: C[m][n] = sum over groups of scale * (sum
+ * of x * code - zero * sum of x), every sum in binary32.  (The kernels sum x *
+ * (code + 24) and take 24 times the sum of x off: a row of X with an infinity or
+ * a NaN gives NaN, and so may one with magnitudes above 2^115.)  Beyond, each
+ * weight is first rounded once to `type`, into the workspace, and the product is
+ * that of 16-bit weights.  M = 0 or N = 0 is a no-op; K = 0 sets C to 0.  X,
+ * codes and C 16-byte aligned, scales and zeros 2-byte.  M is at most
+ * LPGEMM_MAX_M_W4, N at most LPGEMM_MAX_N_W4, with below 2^24 tiles of 64 x 64 of
+ * C (UNSUPPORTED_SHAPE otherwise).
+ * `workspace`, 256-byte aligned, holds at least lpgemm_w4_workspace(M, N, K,
+ * group, 0) bytes (0 up to LPGEMM_W4_SHORT_M rows; -1 for sizes out of range or
+ * no device), which depends on the current device's number of compute units;
  * INVALID_VALUE where it is missing or too small. */
 #define LPGEMM_MAX_STRIDE 2097152
+#define LPGEMM_MAX_M_W4 134217728
+#define LPGEMM_MAX_N_W4 16777216
 #define LPGEMM_W4_SHORT_M 4
 #define LPGEMM_W4_EXACT_M 384
 int64_t lpgemm_w4_workspace(int64_t M, int64_t N, int64_t K, int64_t group, int gated);
@@ -101,7 +106,7 @@ lpgemm_status lpgemm_w4(int64_t M, int64_t N, int64_t K, int64_t group, lpgemm_t
 /* H = act(X . G^T) * (X . U^T), M x F of out_type, where the first F of the 2 F
  * weight rows are G and the others U; both products, the activation and the
  * product of the two in binary32, rounded once.  Otherwise as lpgemm_w4 with
- * N = 2 F. */
+ * N = 2 F (and the workspace of gated = 1). */
 lpgemm_status lpgemm_gated_w4(int64_t M, int64_t F, int64_t K, int64_t group, lpgemm_type type,
                               lpgemm_activation activation, const void *X, int64_t x_stride,
                               const uint8_t *codes, const void *scales, const void *zeros, lpgemm_type out_type,
@@ -143,6 +148,18 @@ lpgemm_status lpgemm_gated_ffn_backward(int64_t M, int64_t D, int64_t F, lpgemm_
                                         const void *W_down, const void *GU, lpgemm_type grad_type, void *dX,
                                         void *dW_gate_up, void *dW_down, void *workspace,
                                         int64_t workspace_bytes, hipStream_t stream);
+
+/* Ablation hook, as lpgemm_force_config: every call takes its kernels by its
+ * sizes; lpgemm_force_ffn_config(c) pins one for every later call in the process
+ * that can run it, or restores the choice for any other value (-1), and returns
+ * the previous setting.  0, 1, 2: the block's products on tiles of 64, 128 and
+ * 256 rows; 3: its forward pass and the 4-bit products on the kernel for few
+ * rows; 4, 5, 6: the 4-bit products on tiles of 32 and 64 rows and through
+ * 16-bit weights (4-bit products of up to LPGEMM_W4_SHORT_M rows stay on the
+ * kernel for few rows).  The sums' order depends on it, and with it the bits of
+ * the results, and how large a workspace has to be: ask after setting it. */
+int lpgemm_ffn_config_count(void);
+int lpgemm_force_ffn_config(int config);
 
 #ifdef __cplusplus
 }

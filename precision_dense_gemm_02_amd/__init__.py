@@ -35,7 +35,8 @@ _MOE = ("add_rmsnorm_quantize", "silu_mul_quantize", "quantize_mxfp4", "dequanti
         "force_grouped_config", "grouped_auto_config")
 # ... and those of 4-bit weights and of the gated feed-forward block
 _FFN = ("quantize_w4", "dequantize_w4", "gemm_w4", "gated_gemm_w4", "gated_ffn", "gated_ffn_backward",
-        "gated_ffn_workspace_bytes", "gated_ffn_backward_workspace_bytes")
+        "w4_workspace_bytes", "gated_ffn_workspace_bytes", "gated_ffn_backward_workspace_bytes", "ffn_config_count",
+        "force_ffn_config")
 __all__ += _MOE + _FFN
 
 

@@ -59,6 +59,17 @@ def _activation(name) -> int:
     return a
 
 
+def ffn_config_count() -> int:
+    """Number of kernels force_ffn_config can pin."""
+    return int(load_library().lpgemm_ffn_config_count())
+
+
+def force_ffn_config(config: int) -> int:
+    """Pin kernel `config` for later calls of these operators in this process
+    (-1: by size); returns the previous setting."""
+    return int(load_library().lpgemm_force_ffn_config(int(config)))
+
+
 def quantize_w4(w, group_size: int = 128, zeros: bool = False, codes_out=None, scales_out=None, zeros_out=None):
     """4-bit codes of weights w, N x K fp16 or bf16 (contiguous rows, a row
     stride that is a multiple of 8), in groups of `group_size` (32, 64, 128 or
@@ -137,6 +148,12 @@ def _scratch(bytes_needed: int, dev, workspace):
     return workspace.data_ptr(), workspace.numel(), workspace
 
 
+def w4_workspace_bytes(M: int, N: int, K: int, group_size: int, gated: bool = False) -> int:
+    """Bytes of scratch that gemm_w4 (gated: gated_gemm_w4, N = 2F) needs on the
+    current device (-1: sizes out of range)."""
+    return _size("lpgemm_w4_workspace", M, N, K, group_size, int(gated))
+
+
 def _w4_scratch(M, N, K, group, gated, dev, workspace):
     if M <= W4_SHORT_M:
         return None, 0, None
@@ -147,8 +164,9 @@ def gemm_w4(x, codes, scales, zeros: Optional[torch.Tensor] = None, out_dtype=No
     """C = x . W^T for 4-bit weights W (N x K, as quantize_w4 makes them) and x,
     M x K fp16 or bf16 of the scales' type (contiguous rows, a row stride that is
     a multiple of 8); C is M x N in `out_dtype` (x's type, or fp32, fp16, bf16).
-    The weights enter the sums exactly, in fp32.  `workspace`: uint8 scratch to
-    use instead of a new allocation (above 64 rows)."""
+    Sums are in fp32; up to 384 rows the weights enter them exactly, beyond each
+    is rounded once to x's type.  `workspace`: uint8 scratch of
+    w4_workspace_bytes(M, N, K, group) to use instead of a new allocation."""
     M, N, K, stride, group, z = _x_and_w4(x, codes, scales, zeros)
     dev, t = x.device, x.dtype
     out_dtype = t if out_dtype is None else _out_dtype(out_dtype)

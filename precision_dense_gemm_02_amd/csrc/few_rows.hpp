@@ -13,8 +13,6 @@ namespace lpgemm {
 template <typename T>
 lpgemm_status run_few_rows(const FewRowsArgs& p, int w4, int cu_count, hipStream_t stream);
 
-extern int g_few_rows_nb, g_few_rows_waves, g_few_rows_lds;
-
 #ifdef LPGEMM_FEW_ROWS_DEFINE
 // The most wavefronts of a workgroup, and the blocks a wavefront has in flight:
 // as many as the registers hold (128 of them for 16 wavefronts, 256 for 8).
@@ -54,7 +52,7 @@ lpgemm_status run_few_rows(const FewRowsArgs& args, int w4, int cu_count, hipStr
   const int blocks = (p.K + 127) / 128;
   p.x_lds_stride = blocks * 256 + 16;
   const int64_t x_lds = (int64_t)p.M * p.x_lds_stride;
-  const bool in_lds = p.M <= 4 && x_lds <= 1024 * g_few_rows_lds;
+  const bool in_lds = p.M <= 4 && x_lds <= 64 * 1024;
   int nb = gated ? 2 : 1, waves = 8;
   const bool many = grid(nb) > cu_count;
   if (in_lds) {
@@ -67,8 +65,6 @@ lpgemm_status run_few_rows(const FewRowsArgs& args, int w4, int cu_count, hipStr
     if (many) nb = 2, waves = 4;
     else if (w4 && tiles(p.M, 32) > 1) nb = 2;
   }
-  if (g_few_rows_nb > 0 && !(gated && g_few_rows_nb == 1) && !(mt > 1 && g_few_rows_nb == 4)) nb = g_few_rows_nb;
-  if (g_few_rows_waves > 0) waves = g_few_rows_waves;
   if (waves > few_rows_waves(mt, nb)) waves = few_rows_waves(mt, nb);
   while (waves > 1 && waves / 2 >= blocks) waves /= 2;
   size_t lds = (size_t)waves * 16 * mt * (16 * nb + 1) * 4;

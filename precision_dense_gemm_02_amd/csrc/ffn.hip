@@ -3,9 +3,8 @@
 #include "few_rows.hpp"
 
 namespace lpgemm {
-int g_few_rows_nb = 0, g_few_rows_waves = 0, g_few_rows_lds = 64;
-}
-extern "C" void lpgemm_tune_few_rows(int nb, int waves, int lds) { lpgemm::g_few_rows_nb = nb; lpgemm::g_few_rows_waves = waves; lpgemm::g_few_rows_lds = lds; }
+std::atomic<int> g_forced_ffn{-1};
+}  // namespace lpgemm
 
 using namespace lpgemm;
 
@@ -27,7 +26,12 @@ bool bad_stride(int64_t stride, int64_t D) { return stride < D || stride % 8 != 
 // small weights (us, both products, few_rows against tiles: 8 x 4096 x 14336 75
 // and 77, 16 rows 85 and 78; 33 x 1024 x 2816 16.2 and 19.6, 64 rows 21.0 and
 // 20.2).
-bool few_rows_forward(int64_t M, int64_t D, int64_t F) { return M <= 8 || (M <= 48 && D * F <= (int64_t)4 << 20); }
+bool few_rows_forward(int64_t M, int64_t D, int64_t F) {
+  const int forced = forced_ffn();
+  if (forced >= FFN_TILE_64 && forced <= FFN_TILE_256) return false;
+  if (forced == FFN_FEW_ROWS) return M <= 16 * 65535;
+  return M <= 8 || (M <= 48 && D * F <= (int64_t)4 << 20);
+}
 
 // The workspace's parts, in bytes from its start.
 struct ForwardSpace {
@@ -202,6 +206,12 @@ lpgemm_status backward(int64_t M, int64_t D, int64_t F, int activation, const vo
 }  // namespace
 
 extern "C" {
+
+int lpgemm_ffn_config_count(void) { return FFN_CONFIG_COUNT; }
+
+int lpgemm_force_ffn_config(int config) {
+  return g_forced_ffn.exchange(config >= 0 && config < FFN_CONFIG_COUNT ? config : -1);
+}
 
 int64_t lpgemm_gated_ffn_workspace(int64_t M, int64_t D, int64_t F) { return workspace_bytes_of<ForwardSpace>(M, D, F); }
 

@@ -9,6 +9,20 @@
 
 namespace lpgemm {
 
+// What lpgemm_force_ffn_config pins.
+enum FfnConfig {
+  FFN_TILE_64 = 0,    // the block's products on 64 x 128 tiles
+  FFN_TILE_128 = 1,   // ... 128 x 128
+  FFN_TILE_256 = 2,   // ... 256 x 256
+  FFN_FEW_ROWS = 3,   // few_rows: the block's forward pass, 4-bit weights
+  FFN_W4_32 = 4,      // 4-bit weights: tiles of 32 rows
+  FFN_W4_64 = 5,      // ... of 64 rows
+  FFN_W4_WHOLE = 6,   // ... through 16-bit weights
+  FFN_CONFIG_COUNT = 7
+};
+extern std::atomic<int> g_forced_ffn;   // (ffn.hip)
+inline int forced_ffn() { return g_forced_ffn.load(std::memory_order_relaxed); }
+
 // The products of the block.
 enum TileJob {
   JOB_GATED = 0,       // [g u] = X . W_gate_up^T, with the activation
@@ -38,12 +52,14 @@ inline TilePlan plan_tiles(int job, int64_t M, int64_t N, int64_t K, int cu_coun
     int bm, bn, per_cu;
     double stage, stage_full, ends;   // a stage with few workgroups and with all places taken, a workgroup's start and end
   };
-  constexpr Tile kTiles[] = {{64, 128, 2, 0.433, 0.96, 4.19}, {128, 128, 2, 0.527, 1.045, 7.51}, {256, 256, 1, 1.033, 1.33, 20.8}};
+  static constexpr Tile kTiles[] = {{64, 128, 2, 0.433, 0.96, 4.19}, {128, 128, 2, 0.527, 1.045, 7.51}, {256, 256, 1, 1.033, 1.33, 20.8}};
   const double end_factor = job == JOB_GATED_GRAD ? 1.71 : job == JOB_GATED ? 1.43 : 1.0;
   const double stages = (double)((K + 63) / 64);
   TilePlan best{64, 128, 1};
   double least = 1e300;
+  const int forced = forced_ffn();
   for (const Tile& t : kTiles) {
+    if (forced >= FFN_TILE_64 && forced <= FFN_TILE_256 && &t != &kTiles[forced]) continue;
     const double count = (double)((M + t.bm - 1) / t.bm) * (double)((N + t.bn - 1) / t.bn), places = (double)cu_count * t.per_cu;
     for (int splits = 1; splits <= 16 && (splits == 1 || 2 * splits <= stages); splits *= 2) {
       const double per_split = (double)(((int64_t)stages + splits - 1) / splits);

@@ -8,6 +8,8 @@
 // gradients read the same arrays the other way).
 #pragma once
 
+#include <utility>
+
 #include "activation.hpp"
 #include "few_rows_kernels.hpp"
 
@@ -135,16 +137,34 @@ __global__ __launch_bounds__(256) void join_splits(TileArgs p) {
   finish8<T, END>(p, row, col, v, u);
 }
 
+template <typename F, int... T>
+__device__ __forceinline__ void for_each_slot(F&& f, std::integer_sequence<int, T...>) {
+  (f(std::integral_constant<int, T>()), ...);
+}
+
+// 16 bytes per lane from buffer offset voff + soff to lds_addr + IMM + 16 lane.
+// (M0 is set in one instruction and not restored, the offset along k travels in
+// a scalar register: three instructions a load instead of nine, which then fit
+// beside the matrix instruction in front of it.)
+template <int IMM>
+__device__ __forceinline__ void lds_dma_16_at(const i32x4& rsrc, uint32_t lds_addr, uint32_t voff, uint32_t soff) {
+  asm volatile(
+      "s_add_u32 m0, %0, %4\n\t"
+      "s_nop 0\n\t"
+      "buffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds_addr), "v"(voff), "s"(rsrc), "s"(soff), "n"(IMM)
+      : "memory", "m0", "scc");
+}
+
 // BM x BN tiles, four waves in a WM x WN grid, rings of SA and SB K-stages of 64
 // for the two operands.  A stage holds an operand's rows of 128 bytes along k, or its 64 k-rows
 // across it; both arrive by 16-byte direct-to-LDS loads, swizzled, and leave
 // as 32 x 16 fragments: one ds_read_b128, or two transposing ds_read_b64.  Lane
 // l has k = 32 (l / 32) + 8 kk .. + 7 of the stage in K-step kk for both.
 //
-// The loads of A's stage s + SA - 1 and B's stage s + SB - 1 go out in the first
-// two K-steps of stage s, one matrix instruction pinned in front of each; one barrier per stage, in its
-// last K-step, publishes stage s + 1, whose first fragments are read while the
-// rest of stage s's products run.
+// The loads of A's stage s + SA - 1 and B's stage s + SB - 1 go out during stage
+// s, spread over its products; one barrier per stage, in its last K-step,
+// publishes stage s + 1, whose first fragments are read while the rest of stage
+// s's products run.  The order of products, reads and loads is pinned.
 //
 // END_GATED: a wave's columns are WTN / 2 of the gate and the same of the up
 // projection, so that both sums of an element meet in one lane.
@@ -228,17 +248,26 @@ __global__ __launch_bounds__(256) void ffn_tile(TileArgs p) {
     if constexpr (A_ACROSS) rsrc_a = across_rsrc(a_base, p.a_stride, sa);
     if constexpr (B_ACROSS) rsrc_b = across_rsrc(b_base, p.b_stride, sb);
   };
-  auto issue_load = [&](int t, int s, int slot) __attribute__((always_inline)) {   // of stage s, into that place of the ring
-    const bool is_a = t < kSlotsA;
-    const uint32_t to = smem_lds + (is_a ? slot * kStageA + (4 * t + wave) * 1024 : kRingB + slot * kStageB + (4 * (t - kSlotsA) + wave) * 1024);
-    uint32_t from = off[t];
-    if (!(is_a ? A_ACROSS : B_ACROSS)) {
-      const uint32_t kbyte = (uint32_t)s * 128;
-      from = s < s_end && kbyte + along_col < row_bytes ? from + kbyte : kOutOfRange;
+  // Along k: a scalar offset, no records past the last stage, and lanes whose
+  // chunk lies behind the row's end in the stage where it ends.  t: the load slot.
+  const uint32_t wave_lds = smem_lds + wave * 1024;
+  auto issue_load = [&](auto t_c, int s, int slot) __attribute__((always_inline)) {   // of stage s, into that place of the ring
+    constexpr int t = decltype(t_c)::value;
+    constexpr bool is_a = t < kSlotsA;
+    constexpr int u = is_a ? t : t - kSlotsA;
+    const uint32_t ring = wave_lds + (is_a ? slot * kStageA : kRingB + slot * kStageB);
+    if constexpr (is_a ? A_ACROSS : B_ACROSS) {
+      lds_dma_16_at<4096 * u>(is_a ? rsrc_a : rsrc_b, ring, off[t], 0);
+    } else {
+      // (past the last stage: no records, and a scalar offset of 0, as the range
+      // check may take it off the records)
+      const uint32_t kbyte = s < s_end ? (uint32_t)s * 128 : 0;
+      const uint32_t from = along_col < row_bytes - kbyte ? off[t] : kOutOfRange;
+      constexpr bool up = !is_a && GATED && (32 * u) % WTN >= WTN / 2;
+      i32x4 rsrc = is_a ? rsrc_a : up ? rsrc_up : rsrc_b;
+      if (s >= s_end) rsrc.z = 0;
+      lds_dma_16_at<4096 * u>(rsrc, ring, from, kbyte);
     }
-    if (is_a) lds_dma_16(rsrc_a, to, from);
-    else if (GATED && (32 * (t - kSlotsA)) % WTN >= WTN / 2) lds_dma_16(rsrc_up, to, from);
-    else lds_dma_16(rsrc_b, to, from);
   };
 
   // fragment addresses of this lane within a stage, in K-step 0
@@ -274,51 +303,43 @@ __global__ __launch_bounds__(256) void ffn_tile(TileArgs p) {
     const u32x2 lo = lds_read_transposed16(at), hi = lds_read_transposed16(at + 8 * bx);
     return i32x4{(int)lo.x, (int)lo.y, (int)hi.x, (int)hi.y};
   };
-  auto read_frags = [&](int slot_a, int slot_b, int kk, int dst) __attribute__((always_inline)) {
+  // fragment n of K-step kk, in the order the products need them: A's first, B's, A's others
+  constexpr int kFrags = TM + TN;
+  auto read_frag = [&](int n, int slot_a, int slot_b, int kk, int dst) __attribute__((always_inline)) {
     const uint8_t* base = smem + Layout::off(fr, 4 * fh + kk);
-#pragma unroll
-    for (int i = 0; i < TM; ++i) {
+    if (n >= 1 && n <= TN) {
+      const int j = n - 1;
+      if constexpr (B_ACROSS) fb[dst][j] = read_across(b_at[j] + slot_b * kStageB + kk * 16 * BN, BN);
+      else fb[dst][j] = *(const i32x4*)(base + kRingB + slot_b * kStageB + (wn * TN + j) * 4096);
+    } else {
+      const int i = n == 0 ? 0 : n - TN;
       if constexpr (A_ACROSS) fa[dst][i] = read_across(a_at[i] + slot_a * kStageA + kk * 16 * BM, BM);
       else fa[dst][i] = *(const i32x4*)(base + slot_a * kStageA + (wm * TM + i) * 4096);
     }
-#pragma unroll
-    for (int j = 0; j < TN; ++j) {
-      if constexpr (B_ACROSS) fb[dst][j] = read_across(b_at[j] + slot_b * kStageB + kk * 16 * BN, BN);
-      else fb[dst][j] = *(const i32x4*)(base + kRingB + slot_b * kStageB + (wn * TN + j) * 4096);
-    }
   };
   constexpr int kMfma = TM * TN, kSplit = kMfma > 8 ? 3 : kMfma > 1 ? kMfma / 2 : 1;
-  constexpr int kReads = TM * (A_ACROSS ? 2 : 1) + TN * (B_ACROSS ? 2 : 1);
-  auto compute = [&](int src, int first, int last) __attribute__((always_inline)) {
-#pragma unroll
-    for (int x = 0; x < kMfma; ++x) {
-      if (x < first || x >= last) continue;
-      acc[x / TN][x % TN] = mfma32<T>(fb[src][x % TN], fa[src][x / TN], acc[x / TN][x % TN]);
-    }
+  auto product = [&](int x, int src) __attribute__((always_inline)) {
+    acc[x / TN][x % TN] = mfma32<T>(fb[src][x % TN], fa[src][x / TN], acc[x / TN][x % TN]);
   };
-  auto interleave = [&](int mfmas, int reads) __attribute__((always_inline)) {
-#pragma unroll
-    for (int x = 0; x < kMfma; ++x) {
-      if (x >= mfmas) break;
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                      // MFMA
-      if (x * kReads < reads * kMfma) __builtin_amdgcn_sched_group_barrier(0x100, (kReads + kMfma - 1) / kMfma, 0);   // DS read
-    }
-  };
-  constexpr int kLoadSteps = 2, kLoadsPerStep = (kSlots + kLoadSteps - 1) / kLoadSteps;
+  auto each_slot = [](auto&& f) __attribute__((always_inline)) { for_each_slot(f, std::make_integer_sequence<int, kSlots>()); };
+  // The loads of a stage are spread over the products of its first three K-steps
+  // (all in front of its wait), a K-step's fragment reads over the first products
+  // of the one before.
+  constexpr int kReadSpan = kMfma > 8 ? kFrags : kMfma;
 
   if (s_begin < s_end) {
 #pragma unroll
     for (int i = 1 - SB; i < 0; ++i) {   // as the stages before the first would have
       enter_stage(s_begin + i + SA - 1, s_begin + i + SB - 1);
-#pragma unroll
-      for (int t = 0; t < kSlots; ++t) {
-        if (t >= kSlotsA) issue_load(t, s_begin + i + SB - 1, i + SB - 1);
-        else if (i + SA - 1 >= 0) issue_load(t, s_begin + i + SA - 1, i + SA - 1);
-      }
+      each_slot([&](auto t_c) __attribute__((always_inline)) {
+        if (decltype(t_c)::value >= kSlotsA) issue_load(t_c, s_begin + i + SB - 1, i + SB - 1);
+        else if (i + SA - 1 >= 0) issue_load(t_c, s_begin + i + SA - 1, i + SA - 1);
+      });
     }
     wait_vmcnt<kInFlight>();
     block_barrier();
-    read_frags(0, 0, 0, 0);
+#pragma unroll
+    for (int n = 0; n < kFrags; ++n) read_frag(n, 0, 0, 0, 0);
     int slot_a = 0, slot_b = 0;
     for (int s = s_begin; s < s_end; ++s) {
       // (past the last stage the loads move no data)
@@ -328,35 +349,32 @@ __global__ __launch_bounds__(256) void ffn_tile(TileArgs p) {
       auto step = [&](auto kk_c) __attribute__((always_inline)) {
         constexpr int kk = decltype(kk_c)::value;
         constexpr int src = kk & 1, dst = src ^ 1;
-        int pre = 0;
-        if constexpr (kk < kLoadSteps) {
-#pragma unroll
-          for (int t = 0; t < kSlots; ++t) {
-            if (t / kLoadsPerStep != kk) continue;
-            if (pre < kMfma) {
-              compute(src, pre, pre + 1);
-              ++pre;
-              __builtin_amdgcn_sched_barrier(0);
-            }
-            issue_load(t, t < kSlotsA ? s + SA - 1 : s + SB - 1, t < kSlotsA ? load_a : load_b);
-            __builtin_amdgcn_sched_barrier(0);
+        // product x, then what goes out behind it
+        auto one = [&](auto x_c) __attribute__((always_inline)) {
+          constexpr int x = decltype(x_c)::value;
+          if constexpr (kk == 3 && x == kSplit) {
+            wait_vmcnt<kInFlight>();   // own loads of stage s + 1 landed
+            wait_lgkmcnt0();           // own reads of stage s done
+            block_barrier();           // ... everyone's
           }
-        }
-        if constexpr (kk < 3) {
-          read_frags(slot_a, slot_b, kk + 1, dst);
-          compute(src, pre, kMfma);
-          interleave(kMfma - pre, kReads);
-        } else {
-          compute(src, 0, kSplit);
-          interleave(kSplit, 0);
+          product(x, src);
+          constexpr int r = kk == 3 ? x - kSplit : x, span = kk == 3 && kReadSpan > kMfma - kSplit ? kMfma - kSplit : kReadSpan;
+          if constexpr (r >= 0 && r < span) {
+#pragma unroll
+            for (int n = r * kFrags / span; n < (r + 1) * kFrags / span; ++n)
+              read_frag(n, kk == 3 ? next_a : slot_a, kk == 3 ? next_b : slot_b, (kk + 1) % 4, dst);
+          }
+          if constexpr (kk < 3)
+            each_slot([&](auto t_c) __attribute__((always_inline)) {
+              constexpr int t = decltype(t_c)::value;
+              // A's in the first K-step, B's in the next two
+              constexpr int per = t < kSlotsA ? kSlotsA : (kSlotsB + 1) / 2, at = t < kSlotsA ? 0 : 1 + (t - kSlotsA) / per, l = t < kSlotsA ? t : (t - kSlotsA) % per;
+              if constexpr (at == kk && (2 * l + 1) * kMfma / (2 * per) == x)
+                issue_load(t_c, t < kSlotsA ? s + SA - 1 : s + SB - 1, t < kSlotsA ? load_a : load_b);
+            });
           __builtin_amdgcn_sched_barrier(0);
-          wait_vmcnt<kInFlight>();   // own loads of stage s + 1 landed
-          wait_lgkmcnt0();           // own reads of stage s done
-          block_barrier();           // ... everyone's
-          read_frags(next_a, next_b, 0, dst);
-          compute(src, kSplit, kMfma);
-          interleave(kMfma - kSplit, kReads);
-        }
+        };
+        for_each_slot(one, std::make_integer_sequence<int, kMfma>());
       };
       step(std::integral_constant<int, 0>());
       step(std::integral_constant<int, 1>());

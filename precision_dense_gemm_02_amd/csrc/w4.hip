@@ -5,11 +5,6 @@
 #include "ffn.hpp"
 #include "w4_tile.hpp"
 
-namespace lpgemm {
-int g_w4_bm = -1, g_w4_splits = 0;
-}
-extern "C" void lpgemm_tune_w4(int bm, int splits) { lpgemm::g_w4_bm = bm; lpgemm::g_w4_splits = splits; }
-
 using namespace lpgemm;
 
 namespace {
@@ -84,11 +79,13 @@ lpgemm_status product(int64_t M, int64_t N, int64_t F, int64_t K, int64_t group,
                       lpgemm_type out_type, void* C, void* workspace, int64_t workspace_bytes, hipStream_t stream) {
   if (bad_group(K, group) || x_stride < K || x_stride % 8 != 0 || x_stride > LPGEMM_MAX_STRIDE)
     return LPGEMM_ERROR_UNSUPPORTED_SHAPE;
-  if (M > INT32_MAX - 256 || N > INT32_MAX - 256 || tiles(M, 16) > 65535) return LPGEMM_ERROR_UNSUPPORTED_SHAPE;
+  if (M > LPGEMM_MAX_M_W4 || N > LPGEMM_MAX_N_W4 || (M + 63) / 64 * ((N + 63) / 64) >= (int64_t)1 << 24)
+    return LPGEMM_ERROR_UNSUPPORTED_SHAPE;
   if (M == 0 || N == 0) return LPGEMM_SUCCESS;
   if (!C || (K > 0 && (!X || !codes || !scales))) return LPGEMM_ERROR_INVALID_VALUE;
   if (!aligned16(C) || (K > 0 && (!aligned16(X) || !aligned16(codes) || !aligned2(scales) || !aligned2(zeros))))
     return LPGEMM_ERROR_MISALIGNED;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return LPGEMM_ERROR_MISALIGNED;
   DeviceInfo dev;
   const lpgemm_status st = current_device(dev);
   if (st != LPGEMM_SUCCESS) return st;
@@ -210,7 +207,7 @@ lpgemm_status lpgemm_dequantize_w4(int64_t N, int64_t K, int64_t group, lpgemm_t
 }
 
 int64_t lpgemm_w4_workspace(int64_t M, int64_t N, int64_t K, int64_t group, int gated) {
-  if (M < 0 || N < 0 || K < 0 || M > INT32_MAX || N > INT32_MAX || bad_group(K, group) || (gated && N % 2 != 0)) return -1;
+  if (M < 0 || N < 0 || K < 0 || M > LPGEMM_MAX_M_W4 || N > LPGEMM_MAX_N_W4 || bad_group(K, group) || (gated && N % 2 != 0)) return -1;
   if (M == 0 || N == 0) return 0;
   DeviceInfo dev;
   if (current_device(dev) != LPGEMM_SUCCESS) return -1;
@@ -222,7 +219,7 @@ lpgemm_status lpgemm_w4(int64_t M, int64_t N, int64_t K, int64_t group, lpgemm_t
                         int64_t x_stride, const uint8_t* codes, const void* scales, const void* zeros,
                         lpgemm_type out_type, void* C, void* workspace, int64_t workspace_bytes, hipStream_t stream) {
   if (M < 0 || N < 0 || K < 0 || group < 0 || M > INT32_MAX || N > INT32_MAX || !is_16bit(type) ||
-      !any_type(out_type))
+      !any_type(out_type) || workspace_bytes < 0)
     return LPGEMM_ERROR_INVALID_VALUE;
   return product(M, N, 0, K, group, type, 0, X, x_stride, codes, scales, zeros, out_type, C, workspace,
                  workspace_bytes, stream);
@@ -233,7 +230,7 @@ lpgemm_status lpgemm_gated_w4(int64_t M, int64_t F, int64_t K, int64_t group, lp
                               const void* scales, const void* zeros, lpgemm_type out_type, void* H, void* workspace,
                               int64_t workspace_bytes, hipStream_t stream) {
   if (M < 0 || F < 0 || K < 0 || group < 0 || M > INT32_MAX || F > INT32_MAX || !is_16bit(type) ||
-      !any_type(out_type) || (activation != LPGEMM_SILU && activation != LPGEMM_GELU))
+      !any_type(out_type) || (activation != LPGEMM_SILU && activation != LPGEMM_GELU) || workspace_bytes < 0)
     return LPGEMM_ERROR_INVALID_VALUE;
   return product(M, 2 * F, F, K, group, type, activation, X, x_stride, codes, scales, zeros, out_type, H, workspace,
                  workspace_bytes, stream);

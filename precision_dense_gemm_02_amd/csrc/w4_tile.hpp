@@ -5,6 +5,7 @@
 
 #include "../../include/lpgemm_ffn.h"
 #include "dispatch.hpp"
+#include "ffn.hpp"
 #include "w4_tile_kernels.hpp"
 
 namespace lpgemm {
@@ -20,8 +21,6 @@ struct W4Plan {
   int splits;
 };
 
-extern int g_w4_bm, g_w4_splits;
-
 // Up to this many rows the weights enter the sums exactly; beyond, they are
 // first written out as 16-bit values, each rounded once.
 constexpr int kW4ExactRows = LPGEMM_W4_EXACT_M;
@@ -33,16 +32,17 @@ inline W4Plan plan_w4(int64_t M, int64_t N, int64_t K, int cu_count) {
   if (M > kW4ExactRows) plan.way = W4_WHOLE;
   else if (M <= LPGEMM_W4_SHORT_M || (M <= 16 && N < 20480) || weights <= (M <= 32 ? (int64_t)20 << 20 : M <= 64 ? (int64_t)8 << 20 : 0))
     plan.way = W4_FEW_ROWS;
-  if (g_w4_bm >= 0) plan.way = g_w4_bm == 0 ? W4_FEW_ROWS : g_w4_bm == 1 ? W4_WHOLE : W4_TILE;
+  const int forced = forced_ffn();
+  if (M > LPGEMM_W4_SHORT_M && forced >= FFN_FEW_ROWS && (forced != FFN_FEW_ROWS || M <= 16 * 65535)) plan.way = forced == FFN_FEW_ROWS ? W4_FEW_ROWS : forced == FFN_W4_WHOLE ? W4_WHOLE : W4_TILE;
   if (plan.way != W4_TILE) return plan;
   if ((int64_t)tiles(M, 32) * tiles(N, 128) > cu_count) plan.bm = 64;
-  if (g_w4_bm >= 32) plan.bm = g_w4_bm;
+  if (forced == FFN_W4_32) plan.bm = 32;
+  if (forced == FFN_W4_64) plan.bm = 64;
   const int64_t n = (int64_t)tiles(M, plan.bm) * tiles(N, 128), stages = tiles(K, 128);
   int64_t s = cu_count / n;
   if (s > stages / 8) s = stages / 8;
   if (s > 16) s = 16;
   if (s > 1) plan.splits = (int)s;
-  if (g_w4_splits > 0) plan.splits = (int)(g_w4_splits < stages ? g_w4_splits : stages);
   return plan;
 }
 

@@ -66,10 +66,21 @@ def w4_values(codes, scales, zeros, group):
     return (unpack(codes).double() - z) * spread(scales, group)
 
 
-def w4_product(x, codes, scales, zeros, group):
-    """(x . W^T, the error of the kernel's binary32 sums)."""
+W4_EXACT_ROWS = 384          # beyond, the weights are rounded to x's type first
+
+
+def w4_product(x, codes, scales, zeros, group, rounded_weights=None):
+    """(x . W^T, the error of the kernel's binary32 sums).  With weights rounded
+    to x's type each is off by at most half a step, |x| . half_step(W) in all, and
+    the sums are of K products of them."""
+    t = x.dtype
     x = x.double()
-    K = x.shape[1]
+    M, K = x.shape
+    if rounded_weights or (rounded_weights is None and M > W4_EXACT_ROWS):
+        w = w4_values(codes, scales, zeros, group)
+        # (code - zero and its product with the scale are rounded to binary32 before that: 2^-23 of the weight)
+        off = half_step(w, t) + 2.0 ** -23 * w.abs()
+        return x @ w.t(), x.abs() @ off.t() + (K + 40) * U * (x.abs() @ (w.abs() + off).t())
     z = torch.zeros_like(scales).double() if zeros is None else zeros.double()
     s = spread(scales, group).abs()
     # x (24 + code) is summed over a group, then (24 + zero) sum x taken off

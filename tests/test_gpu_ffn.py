@@ -60,6 +60,38 @@ def test_backward(M, D, F, dtype, act):
             ref.check(g, w, err, name)
 
 
+@pytest.fixture
+def pinned():
+    """Pins a kernel for the test's calls."""
+    def pin(config):
+        lp.force_ffn_config(config)
+    yield pin
+    lp.force_ffn_config(-1)
+
+
+@pytest.mark.parametrize("config", [0, 1, 2, 3])
+@pytest.mark.parametrize("M,D,F,dtype,act", [(3, 136, 72, BF16, "silu"), (70, 584, 200, F16, "gelu"),
+                                             (300, 264, 520, BF16, "gelu"), (530, 1032, 712, F16, "silu")])
+def test_every_kernel(pinned, config, M, D, F, dtype, act):
+    x, wgu, wd, dy = problem(M, D, F, dtype, key=5)
+    pinned(config)
+    y, gate_up = lp.gated_ffn(x, wgu, wd, activation=act, keep=True)
+    (y64, y_err), (gu64, gu_err) = ref.block(x, wgu, wd, act)
+    ref.check(gate_up, gu64, gu_err, "gate_up")
+    ref.check(y, y64, y_err, "y")
+    got = lp.gated_ffn_backward(dy, x, wgu, wd, gate_up, activation=act, grad_dtype=F32)
+    for name, g, (w, err) in zip(("dx", "dw_gate_up", "dw_down"), got, ref.block_backward(dy, x, wgu, wd, gate_up, act)):
+        ref.check(g, w, err, name)
+
+
+@pytest.mark.parametrize("M,D,F", [(2100, 264, 4200), (1200, 2600, 2304)])
+def test_several_rounds_of_large_tiles(M, D, F):
+    """More 256 x 256 tiles than compute units, and partial ones at both edges."""
+    for dtype in (F16, BF16):
+        test_backward(M, D, F, dtype, "silu")
+        test_forward(M, D, F, dtype, "gelu")
+
+
 @pytest.mark.parametrize("M,D,F,dtype", [(1, 16, 8, F16), (70, 264, 136, BF16), (300, 512, 384, F16)])
 def test_integers_are_exact(M, D, F, dtype):
     """With every sum an integer that binary32 holds, dx, dW and gate_up are

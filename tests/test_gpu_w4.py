@@ -97,6 +97,15 @@ def test_quantize_special_values(dtype):
         assert torch.isfinite(y[0, 32:]).all() and (y[2, :64] == 0).all()
 
 
+@pytest.fixture
+def pinned():
+    """Pins a kernel for the test's calls."""
+    def pin(config):
+        lp.force_ffn_config(config)
+    yield pin
+    lp.force_ffn_config(-1)
+
+
 def test_quantize_strided_rows():
     base = torch.randn(9, 512, generator=gen(2), device="cuda").to(BF16)
     w = base[::2, 64:320]                      # row stride 1024, offset 128 bytes
@@ -113,7 +122,7 @@ def problem(M, N, K, group, zeros, dtype, key=0):
     return x, codes, scales, z
 
 
-ROWS = [1, 2, 15, 16, 17, 32, 33, 64, 65, 100, 128, 129, 257]
+ROWS = [1, 2, 15, 16, 17, 32, 33, 64, 65, 100, 129, 257, 385]
 
 
 @pytest.mark.parametrize("M", ROWS)
@@ -130,11 +139,31 @@ def test_product(M, N, K, group, zeros, dtype):
         ref.check(got, want, err, f"product {t}")
 
 
-@pytest.mark.parametrize("M", [1, 16, 40, 65, 200])
+FEW_ROWS, TILE_32, TILE_64, WHOLE = 3, 4, 5, 6
+
+
+@pytest.mark.parametrize("config", [FEW_ROWS, TILE_32, TILE_64, WHOLE])
+@pytest.mark.parametrize("M,N,K,group,zeros,dtype", [
+    (5, 1, 32, 32, False, F16), (20, 97, 2080, 32, True, BF16), (33, 130, 576, 64, True, F16),
+    (70, 300, 1280, 256, False, BF16), (129, 257, 4224, 128, True, F16), (400, 131, 384, 128, False, BF16)])
+def test_every_kernel(pinned, config, M, N, K, group, zeros, dtype):
+    x, codes, scales, z = problem(M, N, K, group, zeros, dtype)
+    want, err = ref.w4_product(x, codes, scales, z, group, config == WHOLE)
+    pinned(config)
+    ref.check(lp.gemm_w4(x, codes, scales, z, out_dtype=F32), want, err, "product")
+    if N % 2 == 0:
+        h, h_err = ref.gated(want, err, "gelu")
+        ref.check(lp.gated_gemm_w4(x, codes, scales, z, activation="gelu"), h, h_err, "gated")
+
+
+@pytest.mark.parametrize("config", [-1, FEW_ROWS, TILE_32, TILE_64, WHOLE])
+@pytest.mark.parametrize("M", [1, 16, 40, 65, 200, 400])
 @pytest.mark.parametrize("group", [32, 64, 128, 256])
 @pytest.mark.parametrize("dtype", [F16, BF16])
-def test_product_of_integers_is_exact(M, group, dtype):
-    """Small integers and scales of powers of two: every sum is exact."""
+def test_product_of_integers_is_exact(pinned, config, M, group, dtype):
+    """Small integers and scales of powers of two: every sum is exact, and so are
+    weights in 16 bits."""
+    pinned(config)
     g, N, K = gen(M, group), 150, 1792
     x = torch.randint(-4, 5, (M, K), generator=g, device="cuda").to(dtype)
     codes = torch.randint(0, 256, (N, K // 2), generator=g, device="cuda", dtype=torch.uint8)
@@ -145,7 +174,7 @@ def test_product_of_integers_is_exact(M, group, dtype):
         assert torch.equal(lp.gemm_w4(x, codes, scales, zero, out_dtype=F32).double(), want)
 
 
-@pytest.mark.parametrize("M", [1, 5, 16, 31, 48, 64, 65, 130])
+@pytest.mark.parametrize("M", [1, 5, 16, 31, 48, 65, 130, 390])
 @pytest.mark.parametrize("F,K,group,zeros,dtype,act", [
     (1, 32, 32, False, F16, "silu"), (33, 256, 128, False, BF16, "gelu"), (97, 2080, 32, True, F16, "gelu"),
     (200, 640, 64, True, BF16, "silu"), (1405, 512, 256, False, F16, "silu")])
@@ -157,7 +186,7 @@ def test_gated_product(M, F, K, group, zeros, dtype, act):
         ref.check(got, h, err, f"gated {t}")
 
 
-@pytest.mark.parametrize("M", [1, 20, 70])
+@pytest.mark.parametrize("M", [1, 20, 70, 400])
 def test_strided_rows_and_a_column_slice(M):
     x, codes, scales, z = problem(M, 96, 512, 64, True, BF16)
     wide = torch.full((2 * M, 1024), float("nan"), dtype=BF16, device="cuda")
@@ -211,7 +240,7 @@ def test_empty_sizes():
 
 
 def test_equal_calls_give_equal_bits_and_leave_the_rest_alone():
-    for M in (1, 33, 150):
+    for M in (1, 33, 150, 400):
         x, codes, scales, z = problem(M, 200, 1024, 128, True, BF16)
         keep = [t.clone() for t in (x, codes, scales, z)]
         buf = torch.full((M + 2, 200), 3.0, dtype=BF16, device="cuda")
@@ -221,7 +250,7 @@ def test_equal_calls_give_equal_bits_and_leave_the_rest_alone():
         assert all(torch.equal(p, q) for p, q in zip(keep, (x, codes, scales, z)))
 
 
-@pytest.mark.parametrize("M", [1, 100])
+@pytest.mark.parametrize("M", [1, 20, 100, 400])
 def test_captured_into_a_graph_and_on_another_stream(M):
     x, codes, scales, z = problem(M, 384, 1024, 64, True, F16)
     want = lp.gated_gemm_w4(x, codes, scales, z)
@@ -244,7 +273,9 @@ def test_captured_into_a_graph_and_on_another_stream(M):
 
 def test_many_columns_and_long_rows():
     """Column tiles by the hundred, and K split over every wave many times."""
-    for M, N, K, group, dtype in ((1, 20011, 256, 128, BF16), (2, 40, 32768, 128, F16), (16, 8200, 512, 32, F16)):
+    for M, N, K, group, dtype in ((1, 20011, 256, 128, BF16), (2, 40, 32768, 128, F16), (16, 8200, 512, 32, F16),
+                                  (3, 48, 65536, 256, BF16), (24, 6000, 8192, 128, F16), (300, 5000, 4096, 64, BF16),
+                                  (500, 1032, 4096, 128, BF16)):
         x, codes, scales, z = problem(M, N, K, group, False, dtype)
         want, err = ref.w4_product(x, codes, scales, z, group)
         ref.check(lp.gemm_w4(x, codes, scales, z), want, err, (M, N, K))
