@@ -161,10 +161,9 @@ __device__ __forceinline__ void lds_dma_16_at(const i32x4& rsrc, uint32_t lds_ad
 // as 32 x 16 fragments: one ds_read_b128, or two transposing ds_read_b64.  Lane
 // l has k = 32 (l / 32) + 8 kk .. + 7 of the stage in K-step kk for both.
 //
-// The loads of A's stage s + SA - 1 and B's stage s + SB - 1 go out during stage
-// s, spread over its products; one barrier per stage, in its last K-step,
-// publishes stage s + 1, whose first fragments are read while the rest of stage
-// s's products run.  The order of products, reads and loads is pinned.
+// One barrier per stage.  The fragments are read three K-steps ahead of their
+// products, so that neither their latency nor the wait behind the barrier idles
+// the matrix cores; the order of products, reads and loads is pinned.
 //
 // END_GATED: a wave's columns are WTN / 2 of the gate and the same of the up
 // projection, so that both sums of an element meet in one lane.
@@ -181,7 +180,7 @@ __global__ __launch_bounds__(256) void ffn_tile(TileArgs p) {
   constexpr int kLds = kRingB + SB * kStageB;
   static_assert(kLds <= 160 * 1024, "LDS");
   // loads that may be in flight once stage s + 1 has landed: those behind the
-  // later of A's and B's, which go out in stages s + 2 - SA and s + 2 - SB, A's
+  // later of A's and B's, which go out in rounds s + 1 - SA and s + 1 - SB, A's
   // before B's
   static_assert(SB >= SA && SA >= 2, "rings");
   constexpr int kInFlight = (SA - 2) * kSlots + (SB > SA ? kSlotsB : 0);
@@ -290,7 +289,7 @@ __global__ __launch_bounds__(256) void ffn_tile(TileArgs p) {
     b_at[0] = 0;
   }
 
-  i32x4 fa[2][TM], fb[2][TN];
+  i32x4 fa[4][TM], fb[4][TN];   // of four K-steps
   f32x16 acc[TM][TN];
 #pragma unroll
   for (int i = 0; i < TM; ++i)
@@ -305,84 +304,79 @@ __global__ __launch_bounds__(256) void ffn_tile(TileArgs p) {
   };
   // fragment n of K-step kk, in the order the products need them: A's first, B's, A's others
   constexpr int kFrags = TM + TN;
-  auto read_frag = [&](int n, int slot_a, int slot_b, int kk, int dst) __attribute__((always_inline)) {
+  auto read_frag = [&](int n, int slot_a, int slot_b, int kk) __attribute__((always_inline)) {
     const uint8_t* base = smem + Layout::off(fr, 4 * fh + kk);
     if (n >= 1 && n <= TN) {
       const int j = n - 1;
-      if constexpr (B_ACROSS) fb[dst][j] = read_across(b_at[j] + slot_b * kStageB + kk * 16 * BN, BN);
-      else fb[dst][j] = *(const i32x4*)(base + kRingB + slot_b * kStageB + (wn * TN + j) * 4096);
+      if constexpr (B_ACROSS) fb[kk][j] = read_across(b_at[j] + slot_b * kStageB + kk * 16 * BN, BN);
+      else fb[kk][j] = *(const i32x4*)(base + kRingB + slot_b * kStageB + (wn * TN + j) * 4096);
     } else {
       const int i = n == 0 ? 0 : n - TN;
-      if constexpr (A_ACROSS) fa[dst][i] = read_across(a_at[i] + slot_a * kStageA + kk * 16 * BM, BM);
-      else fa[dst][i] = *(const i32x4*)(base + slot_a * kStageA + (wm * TM + i) * 4096);
+      if constexpr (A_ACROSS) fa[kk][i] = read_across(a_at[i] + slot_a * kStageA + kk * 16 * BM, BM);
+      else fa[kk][i] = *(const i32x4*)(base + slot_a * kStageA + (wm * TM + i) * 4096);
     }
   };
-  constexpr int kMfma = TM * TN, kSplit = kMfma > 8 ? 3 : kMfma > 1 ? kMfma / 2 : 1;
-  auto product = [&](int x, int src) __attribute__((always_inline)) {
-    acc[x / TN][x % TN] = mfma32<T>(fb[src][x % TN], fa[src][x / TN], acc[x / TN][x % TN]);
+  constexpr int kMfma = TM * TN;
+  auto product = [&](int x, int kk) __attribute__((always_inline)) {
+    acc[x / TN][x % TN] = mfma32<T>(fb[kk][x % TN], fa[kk][x / TN], acc[x / TN][x % TN]);
   };
   auto each_slot = [](auto&& f) __attribute__((always_inline)) { for_each_slot(f, std::make_integer_sequence<int, kSlots>()); };
-  // The loads of a stage are spread over the products of its first three K-steps
-  // (all in front of its wait), a K-step's fragment reads over the first products
-  // of the one before.
+  // A round: stage s + 1 has landed and everyone has read stage s, whose places
+  // then take stages s + SA and s + SB; K-steps 1, 2, 3 of stage s and 0 of stage
+  // s + 1 run, and the fragments of stage s + 1 are read, three K-steps ahead.
   constexpr int kReadSpan = kMfma > 8 ? kFrags : kMfma;
+  int slot_a = 0, slot_b = 0;   // the places of stage s
+  auto round = [&](int s, auto first_c) __attribute__((always_inline)) {
+    constexpr bool first = decltype(first_c)::value;   // in front of the first stage: no products yet
+    wait_vmcnt<kInFlight>();   // own loads of stage s + 1 landed
+    wait_lgkmcnt0();           // own reads of stage s done
+    block_barrier();           // ... everyone's
+    const int next_a = slot_a == SA - 1 ? 0 : slot_a + 1, next_b = slot_b == SB - 1 ? 0 : slot_b + 1;
+    enter_stage(s + SA, s + SB);   // (past the last stage the loads move no data)
+    auto step = [&](auto j_c) __attribute__((always_inline)) {
+      constexpr int j = decltype(j_c)::value, kk = (j + 1) % 4;
+      // product x, then what goes out behind it
+      auto one = [&](auto x_c) __attribute__((always_inline)) {
+        constexpr int x = decltype(x_c)::value;
+        if constexpr (!first || j == 3) product(x, kk);
+        if constexpr (x < kReadSpan) {
+#pragma unroll
+          for (int n = x * kFrags / kReadSpan; n < (x + 1) * kFrags / kReadSpan; ++n) read_frag(n, next_a, next_b, j);
+        }
+        each_slot([&](auto t_c) __attribute__((always_inline)) {
+          constexpr int t = decltype(t_c)::value;
+          // A's in the first K-step, B's in the next two
+          constexpr int per = t < kSlotsA ? kSlotsA : (kSlotsB + 1) / 2, at = t < kSlotsA ? 0 : 1 + (t - kSlotsA) / per, l = t < kSlotsA ? t : (t - kSlotsA) % per;
+          if constexpr (at == j && (2 * l + 1) * kMfma / (2 * per) == x)
+            issue_load(t_c, t < kSlotsA ? s + SA : s + SB, t < kSlotsA ? slot_a : slot_b);
+        });
+        __builtin_amdgcn_sched_barrier(0);
+      };
+      for_each_slot(one, std::make_integer_sequence<int, kMfma>());
+    };
+    step(std::integral_constant<int, 0>());
+    step(std::integral_constant<int, 1>());
+    step(std::integral_constant<int, 2>());
+    step(std::integral_constant<int, 3>());
+    slot_a = next_a;
+    slot_b = next_b;
+  };
 
   if (s_begin < s_end) {
+    // the loads that the rounds before would have sent
 #pragma unroll
-    for (int i = 1 - SB; i < 0; ++i) {   // as the stages before the first would have
-      enter_stage(s_begin + i + SA - 1, s_begin + i + SB - 1);
+    for (int i = -SB; i < -1; ++i) {
+      enter_stage(s_begin + i + SA, s_begin + i + SB);
       each_slot([&](auto t_c) __attribute__((always_inline)) {
-        if (decltype(t_c)::value >= kSlotsA) issue_load(t_c, s_begin + i + SB - 1, i + SB - 1);
-        else if (i + SA - 1 >= 0) issue_load(t_c, s_begin + i + SA - 1, i + SA - 1);
+        if (decltype(t_c)::value >= kSlotsA) issue_load(t_c, s_begin + i + SB, i + SB);
+        else if (i + SA >= 0) issue_load(t_c, s_begin + i + SA, i + SA);
       });
     }
-    wait_vmcnt<kInFlight>();
-    block_barrier();
-#pragma unroll
-    for (int n = 0; n < kFrags; ++n) read_frag(n, 0, 0, 0, 0);
-    int slot_a = 0, slot_b = 0;
-    for (int s = s_begin; s < s_end; ++s) {
-      // (past the last stage the loads move no data)
-      const int load_a = slot_a == 0 ? SA - 1 : slot_a - 1, next_a = slot_a == SA - 1 ? 0 : slot_a + 1;
-      const int load_b = slot_b == 0 ? SB - 1 : slot_b - 1, next_b = slot_b == SB - 1 ? 0 : slot_b + 1;
-      enter_stage(s + SA - 1, s + SB - 1);
-      auto step = [&](auto kk_c) __attribute__((always_inline)) {
-        constexpr int kk = decltype(kk_c)::value;
-        constexpr int src = kk & 1, dst = src ^ 1;
-        // product x, then what goes out behind it
-        auto one = [&](auto x_c) __attribute__((always_inline)) {
-          constexpr int x = decltype(x_c)::value;
-          if constexpr (kk == 3 && x == kSplit) {
-            wait_vmcnt<kInFlight>();   // own loads of stage s + 1 landed
-            wait_lgkmcnt0();           // own reads of stage s done
-            block_barrier();           // ... everyone's
-          }
-          product(x, src);
-          constexpr int r = kk == 3 ? x - kSplit : x, span = kk == 3 && kReadSpan > kMfma - kSplit ? kMfma - kSplit : kReadSpan;
-          if constexpr (r >= 0 && r < span) {
-#pragma unroll
-            for (int n = r * kFrags / span; n < (r + 1) * kFrags / span; ++n)
-              read_frag(n, kk == 3 ? next_a : slot_a, kk == 3 ? next_b : slot_b, (kk + 1) % 4, dst);
-          }
-          if constexpr (kk < 3)
-            each_slot([&](auto t_c) __attribute__((always_inline)) {
-              constexpr int t = decltype(t_c)::value;
-              // A's in the first K-step, B's in the next two
-              constexpr int per = t < kSlotsA ? kSlotsA : (kSlotsB + 1) / 2, at = t < kSlotsA ? 0 : 1 + (t - kSlotsA) / per, l = t < kSlotsA ? t : (t - kSlotsA) % per;
-              if constexpr (at == kk && (2 * l + 1) * kMfma / (2 * per) == x)
-                issue_load(t_c, t < kSlotsA ? s + SA - 1 : s + SB - 1, t < kSlotsA ? load_a : load_b);
-            });
-          __builtin_amdgcn_sched_barrier(0);
-        };
-        for_each_slot(one, std::make_integer_sequence<int, kMfma>());
-      };
-      step(std::integral_constant<int, 0>());
-      step(std::integral_constant<int, 1>());
-      step(std::integral_constant<int, 2>());
-      step(std::integral_constant<int, 3>());
-      slot_a = next_a;
-      slot_b = next_b;
-    }
+    slot_a = SA - 1;
+    slot_b = SB - 1;
+    round(s_begin - 1, std::true_type());
+    // (the last round's last K-step is of a stage of zeros)
+    for (int s = s_begin; s < s_end; ++s) round(s, std::false_type());
   }
 
   wait_vmcnt<0>();   // (loads past the last stage: LDS is the next workgroup's once this one ends)
