@@ -77,8 +77,8 @@ int64_t workspace_bytes_of(int64_t M, int64_t D, int64_t F) {
 
 template <typename T>
 lpgemm_status forward(int64_t M, int64_t D, int64_t F, int activation, const void* X, int64_t x_stride,
-                      const void* w_gate_up, const void* w_down, void* GU, void* Y, uint8_t* ws, int cu_count,
-                      hipStream_t stream) {
+                      const void* w_gate_up, const void* w_down, void* GU, void* Y, uint8_t* ws, int64_t ws_bytes,
+                      int cu_count, hipStream_t stream) {
   const ForwardSpace space(M, D, F, cu_count);
   uint8_t* const h = ws + space.h;
   lpgemm_status st = LPGEMM_SUCCESS;
@@ -109,6 +109,7 @@ lpgemm_status forward(int64_t M, int64_t D, int64_t F, int activation, const voi
     return run_few_rows<T>(p, 0, cu_count, stream);
   }
   float* const part = reinterpret_cast<float*>(ws + space.part);
+  const int64_t part_bytes = ws_bytes - space.part;
   TileArgs p{};
   p.A = static_cast<const uint8_t*>(X);
   p.B = static_cast<const uint8_t*>(w_gate_up);
@@ -122,7 +123,7 @@ lpgemm_status forward(int64_t M, int64_t D, int64_t F, int activation, const voi
   p.N = (int)(2 * F);
   p.F = (int)F;
   p.K = (int)D;
-  if (F > 0) st = run_tile<T>(JOB_GATED, p, part, cu_count, stream);
+  if (F > 0) st = run_tile<T>(JOB_GATED, p, part, part_bytes, cu_count, stream);
   if (st != LPGEMM_SUCCESS || D == 0) return st;
   TileArgs q{};
   q.A = h;
@@ -133,17 +134,18 @@ lpgemm_status forward(int64_t M, int64_t D, int64_t F, int activation, const voi
   q.M = (int)M;
   q.N = (int)D;
   q.K = (int)F;
-  return run_tile<T>(JOB_DOWN, q, part, cu_count, stream);
+  return run_tile<T>(JOB_DOWN, q, part, part_bytes, cu_count, stream);
 }
 
 template <typename T>
 lpgemm_status backward(int64_t M, int64_t D, int64_t F, int activation, const void* dY, int64_t dy_stride,
                        const void* X, int64_t x_stride, const void* w_gate_up, const void* w_down, const void* GU,
-                       lpgemm_type grad_type, void* dX, void* dw_gate_up, void* dw_down, uint8_t* ws, int cu_count,
-                       hipStream_t stream) {
+                       lpgemm_type grad_type, void* dX, void* dw_gate_up, void* dw_down, uint8_t* ws,
+                       int64_t ws_bytes, int cu_count, hipStream_t stream) {
   const BackwardSpace space(M, D, F, cu_count);
   uint8_t *const dgu = ws + space.dgu, *const h = ws + space.h;
   float* const part = reinterpret_cast<float*>(ws + space.part);
+  const int64_t part_bytes = ws_bytes - space.part;
   const int own_type = kIsF16<T> ? LPGEMM_F16 : LPGEMM_BF16;
   lpgemm_status st = LPGEMM_SUCCESS;
   if (M > 0 && F > 0) {
@@ -159,7 +161,7 @@ lpgemm_status backward(int64_t M, int64_t D, int64_t F, int activation, const vo
     p.M = (int)M;
     p.N = p.F = (int)F;
     p.K = (int)D;
-    st = run_tile<T>(JOB_GATED_GRAD, p, part, cu_count, stream);
+    st = run_tile<T>(JOB_GATED_GRAD, p, part, part_bytes, cu_count, stream);
   }
   if (st == LPGEMM_SUCCESS && dX && M > 0) {
     TileArgs p{};
@@ -172,7 +174,7 @@ lpgemm_status backward(int64_t M, int64_t D, int64_t F, int activation, const vo
     p.M = (int)M;
     p.N = (int)D;
     p.K = (int)(2 * F);
-    st = run_tile<T>(JOB_DX, p, part, cu_count, stream);
+    st = run_tile<T>(JOB_DX, p, part, part_bytes, cu_count, stream);
   }
   if (st == LPGEMM_SUCCESS && dw_gate_up && F > 0) {
     TileArgs p{};
@@ -185,7 +187,7 @@ lpgemm_status backward(int64_t M, int64_t D, int64_t F, int activation, const vo
     p.M = (int)(2 * F);
     p.N = (int)D;
     p.K = (int)M;
-    st = run_tile<T>(JOB_DW, p, part, cu_count, stream);
+    st = run_tile<T>(JOB_DW, p, part, part_bytes, cu_count, stream);
   }
   if (st == LPGEMM_SUCCESS && dw_down && F > 0) {
     TileArgs p{};
@@ -198,7 +200,7 @@ lpgemm_status backward(int64_t M, int64_t D, int64_t F, int activation, const vo
     p.M = (int)D;
     p.N = (int)F;
     p.K = (int)M;
-    st = run_tile<T>(JOB_DW, p, part, cu_count, stream);
+    st = run_tile<T>(JOB_DW, p, part, part_bytes, cu_count, stream);
   }
   return st;
 }
@@ -239,8 +241,8 @@ lpgemm_status lpgemm_gated_ffn(int64_t M, int64_t D, int64_t F, lpgemm_type type
   if (workspace_bytes < ForwardSpace(M, D, F, dev.cu_count).total) return LPGEMM_ERROR_INVALID_VALUE;
   uint8_t* const ws = static_cast<uint8_t*>(workspace);
   return type == LPGEMM_F16
-             ? forward<TypeF16>(M, D, F, activation, X, x_stride, W_gate_up, W_down, GU, Y, ws, dev.cu_count, stream)
-             : forward<TypeBF16>(M, D, F, activation, X, x_stride, W_gate_up, W_down, GU, Y, ws, dev.cu_count, stream);
+             ? forward<TypeF16>(M, D, F, activation, X, x_stride, W_gate_up, W_down, GU, Y, ws, workspace_bytes, dev.cu_count, stream)
+             : forward<TypeBF16>(M, D, F, activation, X, x_stride, W_gate_up, W_down, GU, Y, ws, workspace_bytes, dev.cu_count, stream);
 }
 
 lpgemm_status lpgemm_gated_ffn_backward(int64_t M, int64_t D, int64_t F, lpgemm_type type,
@@ -267,9 +269,9 @@ lpgemm_status lpgemm_gated_ffn_backward(int64_t M, int64_t D, int64_t F, lpgemm_
   uint8_t* const ws = static_cast<uint8_t*>(workspace);
   return type == LPGEMM_F16
              ? backward<TypeF16>(M, D, F, activation, dY, dy_stride, X, x_stride, W_gate_up, W_down, GU, grad_type, dX,
-                                 dW_gate_up, dW_down, ws, dev.cu_count, stream)
+                                 dW_gate_up, dW_down, ws, workspace_bytes, dev.cu_count, stream)
              : backward<TypeBF16>(M, D, F, activation, dY, dy_stride, X, x_stride, W_gate_up, W_down, GU, grad_type, dX,
-                                  dW_gate_up, dW_down, ws, dev.cu_count, stream);
+                                  dW_gate_up, dW_down, ws, workspace_bytes, dev.cu_count, stream);
 }
 
 }  // extern "C"

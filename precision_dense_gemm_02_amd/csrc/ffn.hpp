@@ -85,9 +85,11 @@ inline int64_t split_bytes(const TilePlan& p, int job, int64_t M, int64_t N) {
 }
 
 // Runs a product (its operands, sizes and outputs set in p) with the splits'
-// sums in `part` where the plan has splits.
+// sums in the `part_bytes` at `part` where the plan has splits.  (The plan is
+// made again here: with another kernel pinned since the workspace was measured
+// it may want more, and is refused.)
 template <typename T>
-lpgemm_status run_tile(int job, TileArgs p, float* part, int cu_count, hipStream_t stream);
+lpgemm_status run_tile(int job, TileArgs p, float* part, int64_t part_bytes, int cu_count, hipStream_t stream);
 
 #ifdef LPGEMM_FFN_DEFINE
 template <typename T, bool A_ACROSS, bool B_ACROSS, int END>
@@ -98,9 +100,10 @@ const void* tile_kernel(const TilePlan& plan) {
 }
 
 template <typename T>
-lpgemm_status run_tile(int job, TileArgs p, float* part, int cu_count, hipStream_t stream) {
+lpgemm_status run_tile(int job, TileArgs p, float* part, int64_t part_bytes, int cu_count, hipStream_t stream) {
   if (p.M == 0 || p.N == 0) return LPGEMM_SUCCESS;
   const TilePlan plan = plan_tiles(job, p.M, p.N, p.K, cu_count);
+  if (split_bytes(plan, job, p.M, p.N) > part_bytes) return LPGEMM_ERROR_INVALID_VALUE;
   p.tiles_m = tiles(p.M, plan.bm);
   p.tiles_n = job == JOB_GATED ? tiles(p.F, plan.bn / 2) : tiles(p.N, plan.bn);
   p.k_stages = tiles(p.K, 64);

@@ -54,7 +54,8 @@ struct W4Space {
 };
 
 template <typename T>
-lpgemm_status run_whole(int64_t group, const W4TileArgs& w, uint8_t* ws, float* part, int cu_count, hipStream_t stream) {
+lpgemm_status run_whole(int64_t group, const W4TileArgs& w, uint8_t* ws, int64_t part, int64_t ws_bytes, int cu_count,
+                        hipStream_t stream) {
   const lpgemm_type type = kIsF16<T> ? LPGEMM_F16 : LPGEMM_BF16;
   lpgemm_status st = lpgemm_dequantize_w4(w.N, w.K, group, type, w.W, w.scales, w.zeros, type, ws, stream);
   if (st != LPGEMM_SUCCESS) return st;
@@ -70,7 +71,7 @@ lpgemm_status run_whole(int64_t group, const W4TileArgs& w, uint8_t* ws, float* 
   p.N = w.N;
   p.F = w.F;
   p.K = w.K;
-  return run_tile<T>(w.F > 0 ? JOB_GATED : JOB_DOWN, p, part, cu_count, stream);
+  return run_tile<T>(w.F > 0 ? JOB_GATED : JOB_DOWN, p, reinterpret_cast<float*>(ws + part), ws_bytes - part, cu_count, stream);
 }
 
 // The product, and (F > 0) the gated product.
@@ -133,8 +134,8 @@ lpgemm_status product(int64_t M, int64_t N, int64_t F, int64_t K, int64_t group,
   uint8_t* const ws = static_cast<uint8_t*>(workspace);
   p.part = reinterpret_cast<float*>(ws + space.part);
   if (plan.way == W4_WHOLE)
-    return type == LPGEMM_F16 ? run_whole<TypeF16>(group, p, ws, p.part, dev.cu_count, stream)
-                              : run_whole<TypeBF16>(group, p, ws, p.part, dev.cu_count, stream);
+    return type == LPGEMM_F16 ? run_whole<TypeF16>(group, p, ws, space.part, workspace_bytes, dev.cu_count, stream)
+                              : run_whole<TypeBF16>(group, p, ws, space.part, workspace_bytes, dev.cu_count, stream);
   if (type == LPGEMM_F16)
     return w4 == 1   ? run_w4_tile<TypeF16, 1>(plan, p, stream)
            : w4 == 2 ? run_w4_tile<TypeF16, 2>(plan, p, stream)

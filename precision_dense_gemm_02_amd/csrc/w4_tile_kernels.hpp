@@ -147,20 +147,13 @@ __global__ __launch_bounds__(256 * WK) void w4_tile(W4TileArgs p) {
   }
   const i32x4 rsrc_w = make_rsrc(p.W + (size_t)c0 * p.row_bytes, (uint32_t)cols * p.row_bytes);
   const i32x4 rsrc_up = make_rsrc(p.W + (size_t)(GATED ? p.F + c0 : c0) * p.row_bytes, (uint32_t)cols * p.row_bytes);
-  // scales of this wave's columns: lane l of load t has column l % 32, group (64 t + l) / 32 of the stage
-  uint32_t s_off[kScLoads];
-  bool s_here[kScLoads];
+  // scales of this wave's columns: lane l of load t has column l % 32, group 2 t + l / 32 of the stage
   const bool wave_up = GATED && wn * 32 >= BN / 2;             // (a wave's columns are of one projection)
   const int wave_row0 = weight_row(wn * 32);
   const int wave_cols = max(min(cols - (wn * 32 - (wave_up ? BN / 2 : 0)), 32), 0);
   const i32x4 rsrc_s = make_rsrc(p.scales + (size_t)wave_row0 * p.groups, (uint32_t)wave_cols * p.groups * 2);
   const i32x4 rsrc_z = make_rsrc(p.zeros ? p.zeros + (size_t)wave_row0 * p.groups : p.scales, p.zeros ? (uint32_t)wave_cols * p.groups * 2 : 0);
-#pragma unroll
-  for (int t = 0; t < kScLoads; ++t) {
-    const int i = 64 * t + lane, g = i / 32;
-    s_here[t] = g < kGroups;
-    s_off[t] = 2u * ((uint32_t)(i % 32) * p.groups + g);
-  }
+  const uint32_t s_off = 2u * ((uint32_t)(lane % 32) * p.groups + lane / 32);
   // the group's i-th stage
   auto issue_stage = [&](int i, int at) __attribute__((always_inline)) {
     const int s = s_begin + i * WK + wk;
@@ -180,8 +173,8 @@ __global__ __launch_bounds__(256 * WK) void w4_tile(W4TileArgs p) {
     const int g0 = (s * 128) >> p.group_shift;                  // (a group of 256 is that of two stages)
 #pragma unroll
     for (int t = 0; t < kScLoads; ++t) {
-      const int g = g0 + (64 * t + lane) / 32;
-      const uint32_t from = live && s_here[t] && g < p.groups ? s_off[t] + 2 * g0 : kOutOfRange;
+      const int g = 2 * t + lane / 32;
+      const uint32_t from = live && g < kGroups && g0 + g < p.groups ? s_off + 2 * (g0 + 2 * t) : kOutOfRange;
       lds_dma_2(rsrc_s, own + t * 256, from);
       lds_dma_2(rsrc_z, own + (kScLoads + t) * 256, from);
     }

@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include "../../precision_dense_gemm_02_amd/csrc/half_types.hpp"
+#include "../../precision_dense_gemm_02_amd/csrc/w4_tile_kernels.hpp"
 
 using namespace lpgemm;
 
@@ -49,6 +50,19 @@ __global__ __launch_bounds__(64) void k_transpose_rows(const uint32_t* in, const
   *(u32x4*)(out + 4 * l) = transpose_rows(*(const u32x4*)(in + 4 * l));
 }
 
+// 16-bit values at the byte offsets offset[lane] of 128 values, straight into
+// LDS; out: the 64 words there, which held ones
+__global__ __launch_bounds__(64) void k_dma2(const uint16_t* in, const int* offset, uint32_t* out) {
+  __shared__ __attribute__((aligned(16))) uint32_t lds[64];
+  const int l = threadIdx.x;
+  lds[l] = 0xffffffffu;
+  __syncthreads();
+  lds_dma_2(make_rsrc(in, 256), lds_address((uint8_t*)lds), (uint32_t)offset[l]);
+  wait_vmcnt<0>();
+  __syncthreads();
+  out[l] = lds[l];
+}
+
 int launch1(const void* fn, void** args, hipStream_t s) {
   return hipLaunchKernel(fn, dim3(1), dim3(64), args, 0, s) == hipSuccess ? 0 : 1;
 }
@@ -75,6 +89,11 @@ int probe_read_transposed(int, const uint16_t* in, const int* addr, uint16_t* ou
 int probe_transpose_rows(int, const uint32_t* in, const int* unused, uint32_t* out, hipStream_t s) {
   void* a[] = {&in, &unused, &out};
   return launch1((const void*)&k_transpose_rows, a, s);
+}
+
+int probe_dma2(int, const uint16_t* in, const int* offset, uint32_t* out, hipStream_t s) {
+  void* a[] = {&in, &offset, &out};
+  return launch1((const void*)&k_dma2, a, s);
 }
 
 }  // extern "C"

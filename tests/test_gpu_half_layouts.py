@@ -1,6 +1,7 @@
 """The lane layouts that the 16-bit kernels assume (half_types.hpp), pinned on
 the device one instruction at a time: both matrix instructions in both types,
-the transposing LDS read and the exchange between 16-lane rows.  Each output
+the transposing LDS read, the exchange between 16-lane rows and the two-byte
+loads into LDS.  Each output
 is compared with the plain definition computed on the host."""
 import ctypes
 import os
@@ -23,7 +24,7 @@ def lib():
     if not os.path.exists(PROBES):
         raise RuntimeError(f"{PROBES} is missing: run __graft_entry__.build()")
     lib = ctypes.CDLL(PROBES)
-    for name in ("probe_mfma32", "probe_mfma16", "probe_read_transposed", "probe_transpose_rows"):
+    for name in ("probe_mfma32", "probe_mfma16", "probe_read_transposed", "probe_transpose_rows", "probe_dma2"):
         getattr(lib, name).argtypes = [ctypes.c_int] + [ctypes.c_void_p] * 4
         getattr(lib, name).restype = ctypes.c_int
     return lib
@@ -67,3 +68,15 @@ def test_exchange_between_lane_rows(lib):
     _call(lib.probe_transpose_rows, 0, words.cuda(), torch.zeros(64, dtype=torch.int32, device="cuda"), out)
     rows = words.reshape(4, 16, 4)                   # row, lane of the row, word
     assert torch.equal(out.cpu().reshape(4, 16, 4), rows.permute(2, 1, 0))
+
+
+def test_two_byte_loads_into_lds(lib):
+    """Lane l's value lands in word l, zero-extended; behind the records, zeros."""
+    values = torch.arange(1000, 1128, dtype=torch.int16)
+    g = torch.Generator().manual_seed(2)
+    offset = 2 * torch.randint(0, 128, (64,), generator=g).int()
+    offset[5], offset[40], offset[63] = 256, 4096, -2 ** 31      # out of range
+    out = torch.zeros(64, dtype=torch.int32, device="cuda")
+    _call(lib.probe_dma2, 0, values.cuda(), offset.cuda(), out)
+    want = torch.where((offset >= 0) & (offset < 256), values[(offset.clamp(0, 254) // 2).long()].int(), 0)
+    assert torch.equal(out.cpu(), want)
