@@ -4,8 +4,9 @@ C = A . B with INT8 and packed INT4 operands summed exactly in int32, FP16
 operands summed in FP32, and an INT8 variant with per-row x per-column fp32
 dequantisation; around them, the per-row int8 quantiser of fp16 activations
 (W8A8), the INT4 path through the FP6 E3M2 matrix cores, split-K variants
-for products with few output tiles, and an fp64 GEMM emulated with exact
-INT8 GEMMs.  The work runs in
+for products with few output tiles, an fp64 GEMM emulated with exact INT8
+GEMMs, the operators of a quantised expert layer (_moe.py), and 4-bit weights
+with group scales and the gated feed-forward block (_ffn.py).  The work runs in
 hand-written HIP kernels behind the C ABI of include/lpgemm.h; this package is
 the torch-facing binding (see _binding.py), the in-tree build step (build.py)
 and the seeded input generators (inputs.py).

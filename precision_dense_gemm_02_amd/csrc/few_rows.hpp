@@ -18,10 +18,10 @@ lpgemm_status run_few_rows(const FewRowsArgs& p, int w4, int cu_count, hipStream
 // as many as the registers hold (128 of them for 16 wavefronts, 256 for 8).
 constexpr int few_rows_waves(int mt, int nb) { return mt * nb == 1 ? 16 : 8; }
 constexpr int few_rows_depth(int w4, int mt, int nb, bool x_lds, int waves) {
-  if (x_lds) return w4 ? (nb == 1 ? 4 : 2) : nb == 4 ? 2 : nb == 2 ? 3 : 4;
+  if (x_lds) return w4 ? (nb == 1 ? 4 : 2) : nb == 2 ? 3 : 4;
   if (mt == 2) return w4 ? 1 : 2;
   if (waves == 16) return w4 ? 1 : 3;
-  return nb == 1 ? 3 : nb == 2 ? 2 : w4 ? 1 : 2;
+  return nb == 1 ? 3 : nb == 2 ? 2 : 1;
 }
 template <typename T, int W4, bool ZEROS, int MT, int NB, bool XLDS, int WAVES>
 const void* few_rows_of() {
@@ -29,8 +29,9 @@ const void* few_rows_of() {
 }
 template <typename T, int W4, bool ZEROS, int MT, bool XLDS>
 const void* few_rows_kernel(int nb, int waves) {
-  if constexpr (MT == 1) {
-    if (nb == 4) return few_rows_of<T, W4, ZEROS, MT, 4, XLDS, 8>();
+  if constexpr (MT == 1 && !XLDS) {
+    if constexpr (W4 != 0)
+      if (nb == 4) return few_rows_of<T, W4, ZEROS, MT, 4, XLDS, 8>();
     if (nb == 1 && waves > 8) return few_rows_of<T, W4, ZEROS, MT, 1, XLDS, 16>();
   }
   return nb == 2 ? few_rows_of<T, W4, ZEROS, MT, 2, XLDS, 8>() : few_rows_of<T, W4, ZEROS, MT, 1, XLDS, 8>();
@@ -53,6 +54,10 @@ lpgemm_status run_few_rows(const FewRowsArgs& args, int w4, int cu_count, hipStr
   p.x_lds_stride = blocks * 256 + 16;
   const int64_t x_lds = (int64_t)p.M * p.x_lds_stride;
   const bool in_lds = p.M <= 4 && x_lds <= 64 * 1024;
+  // Column tiles a workgroup takes, and its waves.  With more workgroups than CUs
+  // smaller ones fill them evenly; 4-bit weights then take four tiles, over which
+  // an X fragment's loads and its sum are shared (bf16, 16 x 14336 x 4096, groups
+  // of 64 with zeros: 16.9 us).
   int nb = gated ? 2 : 1, waves = 8;
   const bool many = grid(nb) > cu_count;
   if (in_lds) {

@@ -77,6 +77,15 @@ __device__ __forceinline__ void store_value(uint8_t* C, int out_type, size_t i, 
 // Whole blocks need no check of k: a lane's offset stays, the descriptors'
 // bases move.
 //
+// Bound by the weights' stream with 16-bit weights (1 x 28672 x 4096 46 us, 5.1
+// TB/s, the rate of a large copy).  With 4-bit ones the loads alone run at 4.4
+// TB/s (1 x 14336 x 14336: 23.5 us of 30.9), the scales, 2 bytes from each of 16
+// rows a load, add 4.5 us to them (groups of 64 with zeros 11), and the rest is
+// the codes' way into the matrix instructions.  All of a segment's scales copied
+// into LDS first: 16 x 14336 x 14336 43.0 -> 37.7 us, 1 x 4096 x 14336 11.6 ->
+// 12.5, 16 x 14336 x 512 6.1 -> 8.7; X of 16 rows in LDS, 16 x
+// 14336 x 4096: 18.4 -> 19.9; neither is kept.
+//
 // W4: 0 for 16-bit weights, else the K-steps of 32 that share a scale (1, 2,
 // or 4 for groups of 128 and more).  XLDS: X, a few rows of it, is copied into
 // LDS first, where its fragments cost no vector loads.

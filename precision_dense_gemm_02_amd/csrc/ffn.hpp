@@ -45,8 +45,9 @@ struct TilePlan {
 // loads and its end (which is longer where the end has an activation); splits
 // add a launch and the traffic of their sums.  Its numbers were fitted to the
 // times of every pair at 130 products (M, N and K of blocks of 16 to 4096 rows,
-// D = 1024 to 4096, F = 1416 to 14336, one MI355X).  At these the choice is 1.2%
-// of the product's time behind the best pair on average, 21% at the worst.
+// D = 1024 to 4096, F = 1416 to 14336, one MI355X).  With the kernels as they are
+// now the choice is 1.5% of the product's time behind the best pair on average,
+// 22% at the worst (116 products; a new fit came to the same).
 inline TilePlan plan_tiles(int job, int64_t M, int64_t N, int64_t K, int cu_count) {
   struct Tile {
     int bm, bn, per_cu;

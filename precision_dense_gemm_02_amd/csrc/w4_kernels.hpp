@@ -19,6 +19,10 @@ struct QuantW4Args {
 // division, from one reciprocal per group: with r = RN(1 / s) and q = RN(w r),
 // RN(q + r (w - q s)) is the correctly rounded quotient (Markstein), three
 // operations instead of ten.
+//
+// 14336 x 4096 bf16, groups of 128: 41 us, 3.6 TB/s; the inverse to fp32 41 us,
+// 6.5 TB/s (its output stays in the caches).  The quantisation is bound by its
+// operations on each value, not by memory.
 template <typename T, int LANES, bool ZEROS>
 __global__ __launch_bounds__(256) void quantize_w4_kernel(QuantW4Args p) {
   const uint32_t i = blockIdx.x * 256u + threadIdx.x;

@@ -25,7 +25,11 @@ struct W4Plan {
 // first written out as 16-bit values, each rounded once.
 constexpr int kW4ExactRows = LPGEMM_W4_EXACT_M;
 
-// N: weight rows (gated: both projections').
+// N: weight rows (gated: both projections').  In us, few rows' kernel against the
+// best tiles: 16 x 4096 x 4096 8.7 and 11.5, 16 x 14336 x 4096 18.6 and 19.9, but
+// 16 x 28672 x 4096 30.1 and 22.8; 32 x 4096 x 4096 11.9 and 12.7, but 32 x 4096 x
+// 14336 33.2 and 20.5.  Tiles against 16-bit weights: 32 x 14336 x 4096 21.0 and
+// 59.6, 2048 x 4096 x 4096 577 and 76.
 inline W4Plan plan_w4(int64_t M, int64_t N, int64_t K, int cu_count) {
   const int64_t weights = N * K;
   W4Plan plan{W4_TILE, 32, 1};
