@@ -94,8 +94,8 @@ __global__ __launch_bounds__(256) void join_w4(W4TileArgs p) {
 // another waits for LDS, without more tiles or splits.
 //
 // Bound by the codes' conversion and by LDS latency, not by memory: 32 x 14336 x
-// 4096 bf16, groups of 64 with zeros 21 us (1.5 TB/s; one group of four waves 24);
-// 37 x 2810 x 2080 gated, groups of 32 10 us, of which splits and their join are 3.
+// 4096 bf16, groups of 64 with zeros 21.0 us (1.6 TB/s; with WK = 2 22.3, with one
+// group of four waves 24.4).
 //
 // STEPS: K-steps of 32 that share a scale (1, 2, or 4 for groups of 128 and more).
 template <typename T, int STEPS, int BM, int STAGES, int WK, bool GATED>
