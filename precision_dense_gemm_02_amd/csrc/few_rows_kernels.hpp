@@ -3,6 +3,7 @@
 #pragma once
 
 #include "activation.hpp"
+#include "few_rows_index.hpp"
 #include "half_types.hpp"
 
 namespace lpgemm {
@@ -94,8 +95,8 @@ __global__ __launch_bounds__(64 * WAVES) void few_rows(FewRowsArgs p) {
   static_assert(!XLDS || MT == 1, "a few rows");
   constexpr int kSub = W4 ? 4 / W4 : 1;                 // groups in a block
   constexpr int kLoads = W4 ? 1 : 4;                    // 16-byte loads per weight row and block
-  constexpr int RUN = W4 ? 2 : 1;                       // consecutive blocks a wave takes: whole cache lines of a row
-  constexpr int kScaleLoads = W4 == 1 ? 2 : 1;          // per row and run, four groups each
+  constexpr int RUN = W4 ? kScaleRun : 1;               // consecutive blocks a wave takes: whole cache lines of a row
+  constexpr int kScaleLoads = scale_loads(W4);          // per row and run, four groups each
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int waves = blockDim.x >> 6;
   const int r = lane & 15, q = lane >> 4;
@@ -123,8 +124,8 @@ __global__ __launch_bounds__(64 * WAVES) void few_rows(FewRowsArgs p) {
     z_base[nb] = (const uint8_t*)(p.zeros + row * p.groups);
     const bool row_here = r < row_count(nb);
     w_off[nb] = row_here ? (uint32_t)(r * p.row_bytes + 16 * q) : kOutOfRange;
-    const int g = W4 == 4 ? (q & 1) >> p.group_shift : q;   // (groups past a row's last: of blocks that are not whole, unused)
-    s_off[nb] = row_here ? 2u * (r * p.groups + g) : kOutOfRange;
+    // (groups past a row's last: of a block that is not there, unused)
+    s_off[nb] = row_here ? 2u * (r * p.groups + scale_lane_group(W4, p.group_shift, q)) : kOutOfRange;
   }
   uint32_t x_off[MT];
 #pragma unroll
@@ -169,10 +170,10 @@ __global__ __launch_bounds__(64 * WAVES) void few_rows(FewRowsArgs p) {
 #pragma unroll
       for (int t = 0; t < kScaleLoads; ++t) {
         // groups of 32: those of block t of the run; of 64: two of each block; more: one of each (both may be the same)
-        const int g = W4 == 4 ? (run * 2) >> p.group_shift : W4 == 2 ? run * 4 : (run * 2 + t) * 4;
-        const int bytes = run * 2 < whole ? 0x7FFFFFFF : 0;
+        const int g = scale_first_group(W4, p.group_shift, run, t);
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
+          const int bytes = run * RUN < whole ? scale_records(row_count(nb), p.groups, g) : 0;
           b.s[nb][t] = __builtin_amdgcn_raw_buffer_load_b16(rsrc_of(s_base[nb] + 2 * (size_t)g, bytes), s_off[nb], 0, 0);
           b.z[nb][t] = ZEROS ? __builtin_amdgcn_raw_buffer_load_b16(rsrc_of(z_base[nb] + 2 * (size_t)g, bytes), s_off[nb], 0, 0) : 0;
         }

@@ -1,0 +1,80 @@
+// Walks the scale loads of the kernel for few rows (csrc/few_rows_index.hpp) as
+// its lanes issue them, on the host.
+//
+//   few_rows_index N K group           the bytes behind the scales that lanes
+//                                      would reach without records, then those
+//                                      that they reach with them
+//   few_rows_index all                 every size of a sweep: nothing behind the
+//                                      scales, and every group that a whole
+//                                      block needs loaded by the lane that hands
+//                                      it round
+#include <cstdio>
+#include <cstdlib>
+#include <cstring>
+#include <initializer_list>
+
+#include "../precision_dense_gemm_02_amd/csrc/few_rows_index.hpp"
+
+using namespace lpgemm;
+
+namespace {
+
+struct Walk {
+  long free_past = 0, past = 0;   // bytes behind the array: without records, with them
+  bool right = true;
+};
+
+Walk walk(int N, int K, int group) {
+  const int w4 = group == 32 ? 1 : group == 64 ? 2 : 4, shift = group == 256 ? 1 : 0;
+  const int groups = K / group, whole = K / 128, runs = (whole + kScaleRun - 1) / kScaleRun;
+  const long size = 2l * N * groups;
+  Walk out;
+  for (int row0 = 0; row0 < N; row0 += 16) {
+    const int rows = N - row0 < 16 ? N - row0 : 16;
+    for (int run = 0; run < runs; ++run) {
+      for (int t = 0; t < scale_loads(w4); ++t) {
+        const int first = scale_first_group(w4, shift, run, t);
+        const long base = 2l * row0 * groups + 2l * first;
+        const int records = scale_records(rows, groups, first);
+        for (int r = 0; r < rows; ++r)
+          for (int q = 0; q < 4; ++q) {
+            const long end = 2l * (r * groups + scale_lane_group(w4, shift, q)) + 2;
+            if (base + end - size > out.free_past) out.free_past = base + end - size;
+            if (end <= records && base + end - size > out.past) out.past = base + end - size;
+          }
+      }
+      // the groups of the blocks that are there, from the lane rows that hand them round
+      for (int h = 0; h < kScaleRun; ++h) {
+        const int block = run * kScaleRun + h;
+        if (block >= whole) continue;
+        for (int t = 0; t < 4 / w4; ++t) {
+          const int load = w4 == 1 ? h : 0, from = w4 == 1 ? t : w4 == 2 ? 2 * h + t : h;
+          const int first = scale_first_group(w4, shift, run, load);
+          const int have = first + scale_lane_group(w4, shift, from), want = (128 * block + 32 * w4 * t) / group;
+          for (int r = 0; r < rows; ++r)
+            if (have != want || 2 * (r * groups + have - first) + 2 > scale_records(rows, groups, first)) out.right = false;
+        }
+      }
+    }
+  }
+  return out;
+}
+
+}  // namespace
+
+int main(int argc, char** argv) {
+  if (argc == 4) {
+    const Walk w = walk(atoi(argv[1]), atoi(argv[2]), atoi(argv[3]));
+    printf("%ld %ld %d\n", w.free_past, w.past, w.right);
+    return 0;
+  }
+  if (argc != 2 || strcmp(argv[1], "all") != 0) return 2;
+  long sizes = 0, past = 0, wrong = 0, reached = 0;
+  for (int group = 32; group <= 256; group *= 2)
+    for (int K = group; K <= 4608; K += group)
+      for (int N : {1, 2, 15, 16, 17, 31, 32, 33, 100}) {
+        const Walk w = walk(N, K, group);
+        ++sizes, past += w.past > 0, wrong += !w.right, reached += w.free_past > 0;
+      }
+  printf("sizes %ld past %ld wrong %ld reached %ld\n", sizes, past, wrong, reached);
+}
