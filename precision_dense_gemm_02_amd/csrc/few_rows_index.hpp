@@ -1,5 +1,6 @@
-// Where few_rows (few_rows_kernels.hpp) loads the scales of 4-bit weights: plain
-// arithmetic, in a file of its own for the host's tests.
+// Where few_rows (few_rows_kernels.hpp) loads the scales of 4-bit weights and
+// the rows of X that it copies into LDS: plain arithmetic, in a file of its own
+// for the host's tests.
 #pragma once
 
 namespace lpgemm {
@@ -28,5 +29,9 @@ constexpr int scale_lane_group(int w4, int group_shift, int q) { return w4 == 4 
 constexpr int scale_records(int rows, int groups, int first_group) {
   return rows * groups > first_group ? 2 * (rows * groups - first_group) : 0;
 }
+
+// The row of X that 16-byte chunk i of rows of `chunks` is in (K = 0: there are
+// none, and none is copied).
+constexpr int x_chunk_row(int i, int chunks) { return chunks > 0 ? i / chunks : 0; }
 
 }  // namespace lpgemm

@@ -270,11 +270,11 @@ __global__ __launch_bounds__(64 * WAVES) void few_rows(FewRowsArgs p) {
     // each thread, which is all of them for one row) and are waited for behind.
     const int chunks = blocks * 16;
     auto x_chunk = [&](int i) -> i32x4 {
-      const int row = i / chunks, c = i - row * chunks;
+      const int row = x_chunk_row(i, chunks), c = i - row * chunks;
       return i < rows_x * chunks && 8 * c < p.K ? *(const i32x4*)(x_base + (size_t)row * p.x_stride + 16 * c) : i32x4{0, 0, 0, 0};
     };
     auto put_chunk = [&](int i, const i32x4& v) {
-      const int row = i / chunks, c = i - row * chunks;
+      const int row = x_chunk_row(i, chunks), c = i - row * chunks;
       if (i < rows_x * chunks) *(i32x4*)(smem + row * p.x_lds_stride + 16 * c) = W4 ? code_order(v) : v;
     };
     const int threads = blockDim.x;

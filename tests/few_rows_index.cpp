@@ -1,5 +1,5 @@
-// Walks the scale loads of the kernel for few rows (csrc/few_rows_index.hpp) as
-// its lanes issue them, on the host.
+// Walks the loads of the kernel for few rows (csrc/few_rows_index.hpp) as its
+// lanes issue them, on the host.
 //
 //   few_rows_index N K group           the bytes behind the scales that lanes
 //                                      would reach without records, then those
@@ -8,10 +8,12 @@
 //                                      scales, and every group that a whole
 //                                      block needs loaded by the lane that hands
 //                                      it round
+//   few_rows_index copy K rows threads how often each chunk of X is copied: the
+//                                      least and the most, and chunks besides
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
-#include <initializer_list>
+#include <vector>
 
 #include "../precision_dense_gemm_02_amd/csrc/few_rows_index.hpp"
 
@@ -60,9 +62,34 @@ Walk walk(int N, int K, int group) {
   return out;
 }
 
+// The copy of X into LDS: chunks i of every thread, as the kernel takes them.
+void copy(int K, int rows, int threads) {
+  const int chunks = (K + 127) / 128 * 16, all = rows * chunks;
+  std::vector<int> times(all);
+  int besides = 0;
+  for (int thread = 0; thread < threads; ++thread) {
+    auto take = [&](int i) {
+      const int row = x_chunk_row(i, chunks), c = i - row * chunks;
+      if (i >= all) return;
+      if (row < 0 || row >= rows || c < 0 || c >= chunks) ++besides;
+      else ++times[row * chunks + c];
+    };
+    for (int i = 2 * threads + thread; i < all; i += threads) take(i);
+    take(thread);
+    take(threads + thread);
+  }
+  int least = all ? times[0] : 0, most = 0;
+  for (int n : times) least = n < least ? n : least, most = n > most ? n : most;
+  printf("%d %d %d\n", least, most, besides);
+}
+
 }  // namespace
 
 int main(int argc, char** argv) {
+  if (argc == 5 && strcmp(argv[1], "copy") == 0) {
+    copy(atoi(argv[2]), atoi(argv[3]), atoi(argv[4]));
+    return 0;
+  }
   if (argc == 4) {
     const Walk w = walk(atoi(argv[1]), atoi(argv[2]), atoi(argv[3]));
     printf("%ld %ld %d\n", w.free_past, w.past, w.right);

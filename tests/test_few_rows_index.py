@@ -1,7 +1,8 @@
-"""Where the kernel for few rows loads the scales and zeros of 4-bit weights:
-its index arithmetic (csrc/few_rows_index.hpp) walked on the host, lane by lane.
-No load reaches behind the tensor, whatever its number of blocks, and every
-group is loaded by the lane that hands it round."""
+"""Where the kernel for few rows loads the scales and zeros of 4-bit weights and
+the rows of X: its index arithmetic (csrc/few_rows_index.hpp) walked on the host,
+lane by lane.  No load reaches behind the tensor, whatever its number of blocks,
+and every group is loaded by the lane that hands it round; the copy of X takes
+every chunk once, and of empty rows none, without dividing by their number."""
 import os
 import subprocess
 
@@ -13,7 +14,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 @pytest.fixture(scope="module")
 def walk(tmp_path_factory):
     exe = str(tmp_path_factory.mktemp("few_rows") / "few_rows_index")
-    subprocess.run(["g++", "-O2", "-std=c++17", "-Wall", "-Werror", os.path.join(HERE, "few_rows_index.cpp"), "-o", exe],
+    # (unoptimised: a division whose result nobody uses is made, and traps where it divides by zero)
+    subprocess.run(["g++", "-O0", "-std=c++17", "-Wall", "-Werror", os.path.join(HERE, "few_rows_index.cpp"), "-o", exe],
                    check=True)
     return lambda *a: subprocess.run([exe, *map(str, a)], check=True, capture_output=True, text=True).stdout.split()
 
@@ -34,3 +36,11 @@ def test_sizes_with_and_without_a_last_half_run(walk):
     assert fields["sizes"] == 9 * (144 + 72 + 36 + 18)
     assert fields["reached"] > 0          # the sweep has sizes where it matters
     assert fields["past"] == 0 and fields["wrong"] == 0
+
+
+@pytest.mark.parametrize("threads", [64, 256, 512])
+@pytest.mark.parametrize("K", [0, 8, 128, 136, 4096, 14336])
+def test_rows_of_x_are_copied_once(walk, K, threads):
+    for rows in (1, 2, 4):
+        least, most, besides = map(int, walk("copy", K, rows, threads))
+        assert (least, most, besides) == ((1, 1, 0) if K else (0, 0, 0))
