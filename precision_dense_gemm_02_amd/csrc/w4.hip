@@ -15,6 +15,10 @@ bool aligned2(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0
 bool bad_group(int64_t K, int64_t group) {
   return (group != 32 && group != 64 && group != 128 && group != 256) || K % group != 0 || K > LPGEMM_MAX_K_W4;
 }
+// More rows, columns or tiles of a product than its kernels index.
+bool too_large(int64_t M, int64_t N) {
+  return M > LPGEMM_MAX_M_W4 || N > LPGEMM_MAX_N_W4 || (M + 63) / 64 * ((N + 63) / 64) >= (int64_t)1 << 24;
+}
 int log2_of(int64_t v) { return 63 - __builtin_clzll((unsigned long long)v); }
 
 lpgemm_status enqueue(const void* fn, int64_t grid, void* args, hipStream_t stream) {
@@ -80,8 +84,7 @@ lpgemm_status product(int64_t M, int64_t N, int64_t F, int64_t K, int64_t group,
                       lpgemm_type out_type, void* C, void* workspace, int64_t workspace_bytes, hipStream_t stream) {
   if (bad_group(K, group) || x_stride < K || x_stride % 8 != 0 || x_stride > LPGEMM_MAX_STRIDE)
     return LPGEMM_ERROR_UNSUPPORTED_SHAPE;
-  if (M > LPGEMM_MAX_M_W4 || N > LPGEMM_MAX_N_W4 || (M + 63) / 64 * ((N + 63) / 64) >= (int64_t)1 << 24)
-    return LPGEMM_ERROR_UNSUPPORTED_SHAPE;
+  if (too_large(M, N)) return LPGEMM_ERROR_UNSUPPORTED_SHAPE;
   if (M == 0 || N == 0) return LPGEMM_SUCCESS;
   if (!C || (K > 0 && (!X || !codes || !scales))) return LPGEMM_ERROR_INVALID_VALUE;
   if (!aligned16(C) || (K > 0 && (!aligned16(X) || !aligned16(codes) || !aligned2(scales) || !aligned2(zeros))))
@@ -208,7 +211,7 @@ lpgemm_status lpgemm_dequantize_w4(int64_t N, int64_t K, int64_t group, lpgemm_t
 }
 
 int64_t lpgemm_w4_workspace(int64_t M, int64_t N, int64_t K, int64_t group, int gated) {
-  if (M < 0 || N < 0 || K < 0 || M > LPGEMM_MAX_M_W4 || N > LPGEMM_MAX_N_W4 || bad_group(K, group) || (gated && N % 2 != 0)) return -1;
+  if (M < 0 || N < 0 || K < 0 || too_large(M, N) || bad_group(K, group) || (gated && N % 2 != 0)) return -1;
   if (M == 0 || N == 0) return 0;
   DeviceInfo dev;
   if (current_device(dev) != LPGEMM_SUCCESS) return -1;

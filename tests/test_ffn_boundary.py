@@ -178,6 +178,15 @@ def test_workspace_sizes_out_of_range():
     assert lib.lpgemm_ffn_config_count() == lp.ffn_config_count() == 7
 
 
+TOO_MANY_TILES = [(2 ** 21, 2 ** 15), (2 ** 15, 2 ** 21), (134217728, 512), (4096, 16777216)]   # 2^24 of 64 x 64
+
+
+def test_products_of_too_many_tiles():
+    for M, N in TOO_MANY_TILES:
+        assert call("lpgemm_w4", M=M, N=N) == SHAPE
+        assert call("lpgemm_gated_w4", M=M, F=N // 2) == SHAPE
+
+
 def test_pinned_kernels():
     n = lp.ffn_config_count()
     assert lp.force_ffn_config(n) == -1 and lp.force_ffn_config(2) == -1
@@ -299,3 +308,12 @@ def test_workspace_that_is_too_small(M):
                                            0, None) == INVALID
     torch.cuda.synchronize()
     assert (out == 7).all() and (ws == 0).all()
+
+
+@pytest.mark.gpu
+def test_no_workspace_for_products_that_are_refused():
+    """(On a GPU: without one the size is -1 in any case.)"""
+    for M, N in TOO_MANY_TILES:
+        for gated in (False, True):
+            assert lp.w4_workspace_bytes(M, N, 256, 64, gated) == -1, (M, N)
+            assert lp.w4_workspace_bytes(M - 64, N, 256, 64, gated) > 0, (M, N)
