@@ -100,7 +100,7 @@ def _w4(codes, scales, zeros):
         _refuse(scales, "scales", _HALF, dims=2)
     groups, K = scales.shape[1], 2 * half
     group = K // groups if groups else 128
-    if K % group or group not in GROUPS or group * groups != K:
+    if group not in GROUPS or group * groups != K:      # (a multiple of group, then)
         raise ValueError(f"scales must have K / group columns, group one of {GROUPS}: K = {K}, scales "
                          f"{tuple(scales.shape)}")
     _full(scales, "scales", scales.dtype, (N, groups), codes.device)

@@ -264,6 +264,15 @@ def test_binding_refuses_shapes():
     refused(ValueError, "needs", lp.gated_ffn_backward, *block, needs=(True, True))
 
 
+def test_binding_refuses_more_scales_than_values():
+    """... of which a group would hold none."""
+    for half in (0, 1):
+        codes, scales = gpu(6, half, dtype=torch.uint8), gpu(6, 3)
+        refused(ValueError, "scales must have", lp.dequantize_w4, codes, scales)
+        refused(ValueError, "scales must have", lp.gemm_w4, gpu(4, 2 * half), codes, scales)
+        refused(ValueError, "scales must have", lp.gated_gemm_w4, gpu(4, 2 * half), codes, scales, gpu(6, 3))
+
+
 def test_binding_refuses_columns_that_are_not_adjacent():
     for bad in (torch.zeros(4, 256, dtype=F16)[:, ::2], torch.zeros(128, 4, dtype=F16).t(),
                 torch.zeros(4, 1, dtype=F16).expand(4, 128)):
