@@ -84,8 +84,10 @@ lpgemm_status lpgemm_dequantize_w4(int64_t N, int64_t K, int64_t group, lpgemm_t
  * (code + 24) and take 24 times the sum of x off: a row of X with an infinity or
  * a NaN gives NaN, and so may one with magnitudes above 2^115.)  Beyond, each
  * weight is first rounded once to `type`, into the workspace, and the product is
- * that of 16-bit weights.  M = 0 or N = 0 is a no-op; K = 0 sets C to 0.  X,
- * codes and C 16-byte aligned, scales and zeros 2-byte.  M is at most
+ * that of 16-bit weights; a weight row that may hold values past the type's range
+ * is divided by a power of two before and its sums multiplied by it after, so
+ * that such weights stay finite.  M = 0 or N = 0 is a no-op; K = 0 sets C to 0.
+ * X, codes and C 16-byte aligned, scales and zeros 2-byte.  M is at most
  * LPGEMM_MAX_M_W4, N at most LPGEMM_MAX_N_W4, with below 2^24 tiles of 64 x 64 of
  * C (UNSUPPORTED_SHAPE otherwise).
  * `workspace`, 256-byte aligned, holds at least lpgemm_w4_workspace(M, N, K,

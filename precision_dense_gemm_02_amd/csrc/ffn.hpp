@@ -1,6 +1,7 @@
 // Host side of the block's products: the tile for the sizes and its launch.
 // run_tile<T> is instantiated once per type in its own translation unit
-// (run_ffn_*.hip).
+// (run_ffn_*.hip), and for the products with 4-bit weights, whose sums are
+// multiplied by factors, in two more (run_ffn_factors_*.hip).
 #pragma once
 
 #include "../../include/lpgemm_ffn.h"
@@ -89,18 +90,18 @@ inline int64_t split_bytes(const TilePlan& p, int job, int64_t M, int64_t N) {
 // sums in the `part_bytes` at `part` where the plan has splits.  (The plan is
 // made again here: with another kernel pinned since the workspace was measured
 // it may want more, and is refused.)
-template <typename T>
+template <typename T, bool FACTORS = false>
 lpgemm_status run_tile(int job, TileArgs p, float* part, int64_t part_bytes, int cu_count, hipStream_t stream);
 
 #ifdef LPGEMM_FFN_DEFINE
-template <typename T, bool A_ACROSS, bool B_ACROSS, int END>
+template <typename T, bool A_ACROSS, bool B_ACROSS, int END, bool FACTORS>
 const void* tile_kernel(const TilePlan& plan) {
-  if (plan.bm == 256) return (const void*)&ffn_tile<T, A_ACROSS, B_ACROSS, 256, 256, 2, 2, 2, 3, END>;
-  if (plan.bm == 128) return (const void*)&ffn_tile<T, A_ACROSS, B_ACROSS, 128, 128, 2, 2, 2, 3, END>;
-  return (const void*)&ffn_tile<T, A_ACROSS, B_ACROSS, 64, 128, 2, 2, 3, 3, END>;
+  if (plan.bm == 256) return (const void*)&ffn_tile<T, A_ACROSS, B_ACROSS, 256, 256, 2, 2, 2, 3, END, FACTORS>;
+  if (plan.bm == 128) return (const void*)&ffn_tile<T, A_ACROSS, B_ACROSS, 128, 128, 2, 2, 2, 3, END, FACTORS>;
+  return (const void*)&ffn_tile<T, A_ACROSS, B_ACROSS, 64, 128, 2, 2, 3, 3, END, FACTORS>;
 }
 
-template <typename T>
+template <typename T, bool FACTORS>
 lpgemm_status run_tile(int job, TileArgs p, float* part, int64_t part_bytes, int cu_count, hipStream_t stream) {
   if (p.M == 0 || p.N == 0) return LPGEMM_SUCCESS;
   const TilePlan plan = plan_tiles(job, p.M, p.N, p.K, cu_count);
@@ -113,12 +114,19 @@ lpgemm_status run_tile(int job, TileArgs p, float* part, int64_t part_bytes, int
   p.part = part;
   p.part_stride = (int)part_stride(job, p.N);
   const void *fn, *join;
-  switch (job) {
-    case JOB_GATED: fn = tile_kernel<T, false, false, END_GATED>(plan), join = (const void*)&join_splits<T, END_GATED>; break;
-    case JOB_DOWN: fn = tile_kernel<T, false, false, END_STORE>(plan), join = (const void*)&join_splits<T, END_STORE>; break;
-    case JOB_GATED_GRAD: fn = tile_kernel<T, false, true, END_GATED_GRAD>(plan), join = (const void*)&join_splits<T, END_GATED_GRAD>; break;
-    case JOB_DX: fn = tile_kernel<T, false, true, END_STORE>(plan), join = (const void*)&join_splits<T, END_STORE>; break;
-    default: fn = tile_kernel<T, true, true, END_STORE>(plan), join = (const void*)&join_splits<T, END_STORE>; break;
+  auto take = [&](auto a_across, auto b_across, auto end) {
+    fn = tile_kernel<T, decltype(a_across)::value, decltype(b_across)::value, decltype(end)::value, FACTORS>(plan);
+    join = (const void*)&join_splits<T, decltype(end)::value, FACTORS>;
+  };
+  constexpr std::false_type along;
+  constexpr std::integral_constant<int, END_STORE> store;
+  if (job == JOB_GATED) take(along, along, std::integral_constant<int, END_GATED>());
+  else if (FACTORS || job == JOB_DOWN) take(along, along, store);   // (4-bit weights lie along k)
+  else if constexpr (!FACTORS) {
+    constexpr std::true_type across;
+    if (job == JOB_GATED_GRAD) take(along, across, std::integral_constant<int, END_GATED_GRAD>());
+    else if (job == JOB_DX) take(along, across, store);
+    else take(across, across, store);
   }
   void* kargs[] = {&p};
   if (hipLaunchKernel(fn, dim3((unsigned)(p.tiles_m * p.tiles_n), (unsigned)plan.splits), dim3(256), kargs, 0, stream) != hipSuccess)

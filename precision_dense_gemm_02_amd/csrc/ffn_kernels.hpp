@@ -41,6 +41,7 @@ struct TileArgs {
   float* part;             // splits > 1: splits x M x part_stride sums (END_GATED: the up projection's in the second half)
   int part_stride;
   int tiles_m, tiles_n;
+  const float* factors;    // FACTORS: what column n's sums are multiplied by first (END_GATED: the up projection's from part_stride / 2 on)
 };
 
 // Chunk position of 16-byte chunk `c` in a stage row k of an operand that lies
@@ -89,10 +90,21 @@ __device__ __forceinline__ void finish8_grad(const TileArgs& p, int row, int col
   *(i32x4*)(p.H + 2 * ((size_t)row * p.F + col)) = narrow8<T>(h);
 }
 
+// (places up to the next multiple of eight columns hold a factor, too)
+__device__ __forceinline__ void multiply8(float (&v)[8], const float* factors) {
+  const f32x4 a = *(const f32x4*)factors, b = *(const f32x4*)(factors + 4);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] *= a[e], v[4 + e] *= b[e];
+}
+
 // Eight consecutive columns of one row: what END does with them.  `v`: the sums
 // (END_GATED: of the gate), `u`: those of the up projection.
-template <typename T, int END>
-__device__ __forceinline__ void finish8(const TileArgs& p, int row, int col, const float (&v)[8], const float (&u)[8]) {
+template <typename T, int END, bool FACTORS>
+__device__ __forceinline__ void finish8(const TileArgs& p, int row, int col, float (&v)[8], float (&u)[8]) {
+  if constexpr (FACTORS) {
+    multiply8(v, p.factors + col);
+    if constexpr (END == END_GATED) multiply8(u, p.factors + p.part_stride / 2 + col);
+  }
   if constexpr (END == END_STORE) {
     store_columns(p.C, p.out_type, row, col, p.N, v);
   } else if constexpr (END == END_GATED) {
@@ -112,7 +124,7 @@ __device__ __forceinline__ void finish8(const TileArgs& p, int row, int col, con
 }
 
 // The splits' sums added in order, eight columns per lane.
-template <typename T, int END>
+template <typename T, int END, bool FACTORS>
 __global__ __launch_bounds__(256) void join_splits(TileArgs p) {
   const int columns = END == END_GATED ? p.F : p.N;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -134,7 +146,7 @@ __global__ __launch_bounds__(256) void join_splits(TileArgs p) {
       }
     }
   }
-  finish8<T, END>(p, row, col, v, u);
+  finish8<T, END, FACTORS>(p, row, col, v, u);
 }
 
 template <typename F, int... T>
@@ -177,7 +189,13 @@ __device__ __forceinline__ void lds_dma_16_at(const i32x4& rsrc, uint32_t lds_ad
 //
 // END_GATED: a wave's columns are WTN / 2 of the gate and the same of the up
 // projection, so that both sums of an element meet in one lane.
-template <typename T, bool A_ACROSS, bool B_ACROSS, int BM, int BN, int WM, int WN, int SA, int SB, int END>
+//
+// FACTORS: B's rows were divided by powers of two (4-bit weights); the sums are
+// multiplied by them again.  A choice at compile time, in translation units of
+// their own: a test of the pointer at run time costs every other product 1 to 5%
+// (forward 1024 x 2048 x 5632 86.6 -> 90.8 us), and the same code object its
+// neighbours up to 4% (backward of that size 210 -> 218).
+template <typename T, bool A_ACROSS, bool B_ACROSS, int BM, int BN, int WM, int WN, int SA, int SB, int END, bool FACTORS>
 __global__ __launch_bounds__(256) void ffn_tile(TileArgs p) {
   using Layout = RowLayout<128>;
   constexpr int WTM = BM / WM, WTN = BN / WN;
@@ -442,7 +460,7 @@ __global__ __launch_bounds__(256) void ffn_tile(TileArgs p) {
       } else if constexpr (END == END_GATED_GRAD) {
         finish8_grad<T>(p, row, col, v, kept[2 * c], kept[2 * c + 1]);
       } else {
-        finish8<T, END>(p, row, col, v, u);
+        finish8<T, END, FACTORS>(p, row, col, v, u);
       }
     }
   }

@@ -3,5 +3,5 @@
 #include "ffn.hpp"
 
 namespace lpgemm {
-template lpgemm_status run_tile<TypeF16>(int, TileArgs, float*, int64_t, int, hipStream_t);
+template lpgemm_status run_tile<TypeF16, false>(int, TileArgs, float*, int64_t, int, hipStream_t);
 }

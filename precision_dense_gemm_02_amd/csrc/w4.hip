@@ -47,22 +47,22 @@ const void* dequantize_kernel(lpgemm_type out) {
 }
 
 // The workspace of a plan, in bytes from its start: W4_WHOLE the weights in 16
-// bits and the splits' sums, W4_TILE the splits' sums.
+// bits, their rows' factors and the splits' sums, W4_TILE the splits' sums.
 struct W4Space {
-  int64_t part, total;
+  int64_t factors, part, total;
   W4Space(const W4Plan& plan, int64_t M, int64_t N, int64_t F, int64_t K, int cu_count) {
-    part = plan.way == W4_WHOLE ? (2 * N * K + 255) / 256 * 256 : 0;
     const int job = F > 0 ? JOB_GATED : JOB_DOWN;
+    factors = plan.way == W4_WHOLE ? (2 * N * K + 255) / 256 * 256 : 0;
+    part = plan.way == W4_WHOLE && K > 0 ? factors + (4 * part_stride(job, N) + 255) / 256 * 256 : factors;
     total = part + (plan.way == W4_WHOLE ? split_bytes(plan_tiles(job, M, N, K, cu_count), job, M, N) : w4_part_bytes(plan, M, N));
   }
 };
 
 template <typename T>
-lpgemm_status run_whole(int64_t group, const W4TileArgs& w, uint8_t* ws, int64_t part, int64_t ws_bytes, int cu_count,
-                        hipStream_t stream) {
-  const lpgemm_type type = kIsF16<T> ? LPGEMM_F16 : LPGEMM_BF16;
-  lpgemm_status st = lpgemm_dequantize_w4(w.N, w.K, group, type, w.W, w.scales, w.zeros, type, ws, stream);
-  if (st != LPGEMM_SUCCESS) return st;
+lpgemm_status run_whole(int64_t group, const W4TileArgs& w, uint8_t* ws, const W4Space& space, int64_t ws_bytes,
+                        int cu_count, hipStream_t stream) {
+  const int job = w.F > 0 ? JOB_GATED : JOB_DOWN;
+  float *const factors = reinterpret_cast<float*>(ws + space.factors), *const part = reinterpret_cast<float*>(ws + space.part);
   TileArgs p{};
   p.A = w.X;
   p.B = ws;
@@ -75,7 +75,25 @@ lpgemm_status run_whole(int64_t group, const W4TileArgs& w, uint8_t* ws, int64_t
   p.N = w.N;
   p.F = w.F;
   p.K = w.K;
-  return run_tile<T>(w.F > 0 ? JOB_GATED : JOB_DOWN, p, reinterpret_cast<float*>(ws + part), ws_bytes - part, cu_count, stream);
+  if (w.K == 0) return run_tile<T>(job, p, part, ws_bytes - space.part, cu_count, stream);   // an empty sum
+  p.factors = factors;
+  RowsW4Args r{};
+  r.codes = w.W;
+  r.scales = w.scales;
+  r.zeros = w.zeros;
+  r.Y = ws;
+  r.factors = factors;
+  r.F = w.F > 0 ? w.F : w.N;
+  r.rows_padded = (int)part_stride(job, w.N);
+  r.rows_up = w.F > 0 ? r.rows_padded / 2 : r.rows_padded;
+  r.chunks = w.K / 8;
+  r.groups = w.groups;
+  r.lanes_log2 = log2_of(group / 8);
+  void* kargs[] = {&r};
+  if (hipLaunchKernel((const void*)&rows_w4_kernel<T>, dim3((unsigned)tiles(r.rows_padded, 4), (unsigned)tiles(r.chunks, 512)),
+                      dim3(256), kargs, 0, stream) != hipSuccess)
+    return LPGEMM_ERROR_LAUNCH;
+  return run_tile<T, true>(job, p, part, ws_bytes - space.part, cu_count, stream);
 }
 
 // The product, and (F > 0) the gated product.
@@ -137,8 +155,8 @@ lpgemm_status product(int64_t M, int64_t N, int64_t F, int64_t K, int64_t group,
   uint8_t* const ws = static_cast<uint8_t*>(workspace);
   p.part = reinterpret_cast<float*>(ws + space.part);
   if (plan.way == W4_WHOLE)
-    return type == LPGEMM_F16 ? run_whole<TypeF16>(group, p, ws, space.part, workspace_bytes, dev.cu_count, stream)
-                              : run_whole<TypeBF16>(group, p, ws, space.part, workspace_bytes, dev.cu_count, stream);
+    return type == LPGEMM_F16 ? run_whole<TypeF16>(group, p, ws, space, workspace_bytes, dev.cu_count, stream)
+                              : run_whole<TypeBF16>(group, p, ws, space, workspace_bytes, dev.cu_count, stream);
   if (type == LPGEMM_F16)
     return w4 == 1   ? run_w4_tile<TypeF16, 1>(plan, p, stream)
            : w4 == 2 ? run_w4_tile<TypeF16, 2>(plan, p, stream)

@@ -225,6 +225,57 @@ def test_scales_and_zeros_of_any_value(M):
     assert not torch.isfinite(out[:, 5]).any() and torch.isnan(out[:, 6]).all()
 
 
+def test_scales_and_zeros_of_any_value_over_many_rows():
+    test_scales_and_zeros_of_any_value(400)
+
+
+def weights_past_the_range(x, codes, scales, zeros, group):
+    """As ref.w4_product with weights rounded to x's type, for rows that hold
+    weights past its range: those are rounded after the row is divided by a power
+    of two, at most 4 times what brings max |scale| (|zero| + 8) to the largest
+    power in range.  Fp16 values below its normal ones then lie 2^-24 2^e apart:
+    half of that is at most 2^-25 (4 most / 2^15) = 2^-38 most."""
+    w = ref.w4_values(codes, scales, zeros, group)
+    most = (scales.double().abs() * (zeros.double().abs() + 8)).amax(1, keepdim=True)
+    off = w.abs() * torch.finfo(x.dtype).eps / 2 + 2.0 ** -38 * most + 2.0 ** -23 * w.abs()
+    x = x.double()
+    return x @ w.t(), x.abs() @ off.t() + (x.shape[1] + 40) * ref.U * (x.abs() @ (w.abs() + off).t())
+
+
+@pytest.mark.parametrize("config", [-1, 0, 1, 2])
+@pytest.mark.parametrize("M,N,K,group,dtype", [(400, 70, 512, 64, F16), (385, 130, 8192, 128, F16), (520, 48, 2080, 32, BF16),
+                                               (391, 62, 768, 256, BF16)])
+def test_weights_past_the_range_of_their_type(pinned, config, M, N, K, group, dtype):
+    """(code - zero) scale may leave x's type (and binary32): the sums stay what
+    they are, for one row as for many."""
+    x, codes, scales, z = problem(M, N, K, group, True, dtype)
+    large, zero = (60000.0, 30000.0) if dtype is F16 else (2.0e38, 1.0e30)
+    x = (x.double() * (2.0 ** -10 if dtype is F16 else 2.0 ** -110)).to(dtype)
+    scales[3], scales[N // 2 + 1] = large, -large         # every weight of the row
+    scales[7, 1] = large                                  # a group of it
+    z[9, -1], z[10] = -zero, 6.0
+    scales[9, -1] = 40.0 if dtype is F16 else 1.0e9
+    scales[11] = 2000.0 if dtype is F16 else 1.0e37       # near the end of the range
+    values = ref.w4_values(codes, scales, z, group)
+    assert (values.abs() > torch.finfo(dtype).max).sum() > 1.5 * K
+    pinned(config)
+    want, err = weights_past_the_range(x, codes, scales, z, group)
+    got = lp.gemm_w4(x, codes, scales, z, out_dtype=F32)
+    assert torch.isfinite(got).all()
+    ref.check(got, want, err, "many rows")
+    few = lp.gemm_w4(x[:3], codes, scales, z, out_dtype=F32)
+    ref.check(few, *ref.w4_product(x[:3], codes, scales, z, group, False), "few rows")
+    if dtype is F16:
+        h, h_err = ref.gated(want, err, "silu")
+        ref.check(lp.gated_gemm_w4(x, codes, scales, z, out_dtype=F32), h, h_err, "gated")
+
+
+def test_no_values_over_many_rows():
+    e = torch.empty(400, 0, dtype=F16, device="cuda"), *(torch.empty(16, 0, dtype=t, device="cuda") for t in (torch.uint8, F16))
+    assert not lp.gemm_w4(*e, out=torch.full((400, 16), 7.0, dtype=F16, device="cuda")).any()
+    assert not lp.gated_gemm_w4(*e, out=torch.full((400, 8), 7.0, dtype=F16, device="cuda")).any()
+
+
 def test_empty_sizes():
     x, codes, scales, _ = problem(4, 16, 64, 32, False, F16)
     assert lp.gemm_w4(x[:0], codes, scales).shape == (0, 16)
