@@ -22,13 +22,13 @@ constexpr int scale_first_group(int w4, int group_shift, int run, int t) {
 // The group that lane row q holds, from the load's first (w4 = 4: one per block).
 constexpr int scale_lane_group(int w4, int group_shift, int q) { return w4 == 4 ? (q & 1) >> group_shift : q; }
 
-// The bytes of `rows` weight rows' scales from the load's first group on: the
-// records of its descriptor.  The last run of an odd number of whole blocks has
-// no second block: its lanes reach past their row's last group, into the next
-// row's or, behind the last row, past the records, where a load gives 0.
-constexpr int scale_records(int rows, int groups, int first_group) {
-  return rows * groups > first_group ? 2 * (rows * groups - first_group) : 0;
-}
+// The last run of an odd number of whole blocks has no second block, whose
+// groups would lie behind their row's last and, in the last row, behind the
+// scales.  Whether the load has a block at all (w4 = 1: load t is block t's) ...
+constexpr bool scale_load_there(int w4, int run, int t, int whole) { return run * kScaleRun + (w4 == 1 ? t : 0) < whole; }
+// ... and whether lane row q's group is that of the run's second block, and is
+// loaded only where that block is there.
+constexpr bool scale_second_block(int w4, int q) { return w4 == 4 ? (q & 1) != 0 : w4 == 2 && q >= 2; }
 
 // The row of X that 16-byte chunk i of rows of `chunks` is in (K = 0: there are
 // none, and none is copied).

@@ -76,7 +76,10 @@ __device__ __forceinline__ void store_value(uint8_t* C, int out_type, size_t i, 
 // groups and hand them round.
 //
 // Whole blocks need no check of k: a lane's offset stays, the descriptors'
-// bases move.
+// bases move.  Only the last run of an odd number of them takes its second
+// block's lanes out of the scales' loads (few_rows_index.hpp): a mask of the
+// offsets, 0.4% of the time of 120 products of 1 to 24 rows; records that end with
+// the rows' scales, in scalar registers that some kernels do not have, 1.0%.
 //
 // Bound by the weights' stream with 16-bit weights (1 x 28672 x 4096 46 us, 5.1
 // TB/s, the rate of a large copy).  With 4-bit ones the loads alone run at 4.4
@@ -124,9 +127,9 @@ __global__ __launch_bounds__(64 * WAVES) void few_rows(FewRowsArgs p) {
     z_base[nb] = (const uint8_t*)(p.zeros + row * p.groups);
     const bool row_here = r < row_count(nb);
     w_off[nb] = row_here ? (uint32_t)(r * p.row_bytes + 16 * q) : kOutOfRange;
-    // (groups past a row's last: of a block that is not there, unused)
     s_off[nb] = row_here ? 2u * (r * p.groups + scale_lane_group(W4, p.group_shift, q)) : kOutOfRange;
   }
+  const uint32_t second_block = scale_second_block(W4, q) ? kOutOfRange : 0;
   uint32_t x_off[MT];
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) x_off[mt] = 16 * mt + r < rows_x ? (uint32_t)((16 * mt + r) * p.x_stride + 16 * q) : kOutOfRange;
@@ -171,11 +174,13 @@ __global__ __launch_bounds__(64 * WAVES) void few_rows(FewRowsArgs p) {
       for (int t = 0; t < kScaleLoads; ++t) {
         // groups of 32: those of block t of the run; of 64: two of each block; more: one of each (both may be the same)
         const int g = scale_first_group(W4, p.group_shift, run, t);
+        const int bytes = scale_load_there(W4, run, t, whole) ? 0x7FFFFFFF : 0;
+        const uint32_t not_there = W4 == 1 || run * RUN + 1 < whole ? 0 : second_block;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-          const int bytes = run * RUN < whole ? scale_records(row_count(nb), p.groups, g) : 0;
-          b.s[nb][t] = __builtin_amdgcn_raw_buffer_load_b16(rsrc_of(s_base[nb] + 2 * (size_t)g, bytes), s_off[nb], 0, 0);
-          b.z[nb][t] = ZEROS ? __builtin_amdgcn_raw_buffer_load_b16(rsrc_of(z_base[nb] + 2 * (size_t)g, bytes), s_off[nb], 0, 0) : 0;
+          const uint32_t off = s_off[nb] | not_there;
+          b.s[nb][t] = __builtin_amdgcn_raw_buffer_load_b16(rsrc_of(s_base[nb] + 2 * (size_t)g, bytes), off, 0, 0);
+          b.z[nb][t] = ZEROS ? __builtin_amdgcn_raw_buffer_load_b16(rsrc_of(z_base[nb] + 2 * (size_t)g, bytes), off, 0, 0) : 0;
         }
       }
     }

@@ -2,8 +2,8 @@
 // lanes issue them, on the host.
 //
 //   few_rows_index N K group           the bytes behind the scales that lanes
-//                                      would reach without records, then those
-//                                      that they reach with them
+//                                      would reach if each run had two blocks,
+//                                      then those that they reach
 //   few_rows_index all                 every size of a sweep: nothing behind the
 //                                      scales, and every group that a whole
 //                                      block needs loaded by the lane that hands
@@ -22,9 +22,13 @@ using namespace lpgemm;
 namespace {
 
 struct Walk {
-  long free_past = 0, past = 0;   // bytes behind the array: without records, with them
+  long free_past = 0, past = 0;   // bytes behind the array: with two blocks in every run, as loaded
   bool right = true;
 };
+
+bool loaded(int w4, int run, int t, int q, int whole) {
+  return scale_load_there(w4, run, t, whole) && (w4 == 1 || run * kScaleRun + 1 < whole || !scale_second_block(w4, q));
+}
 
 Walk walk(int N, int K, int group) {
   const int w4 = group == 32 ? 1 : group == 64 ? 2 : 4, shift = group == 256 ? 1 : 0;
@@ -37,12 +41,11 @@ Walk walk(int N, int K, int group) {
       for (int t = 0; t < scale_loads(w4); ++t) {
         const int first = scale_first_group(w4, shift, run, t);
         const long base = 2l * row0 * groups + 2l * first;
-        const int records = scale_records(rows, groups, first);
         for (int r = 0; r < rows; ++r)
           for (int q = 0; q < 4; ++q) {
-            const long end = 2l * (r * groups + scale_lane_group(w4, shift, q)) + 2;
-            if (base + end - size > out.free_past) out.free_past = base + end - size;
-            if (end <= records && base + end - size > out.past) out.past = base + end - size;
+            const long past = base + 2l * (r * groups + scale_lane_group(w4, shift, q)) + 2 - size;
+            if (past > out.free_past) out.free_past = past;
+            if (loaded(w4, run, t, q, whole) && past > out.past) out.past = past;
           }
       }
       // the groups of the blocks that are there, from the lane rows that hand them round
@@ -53,8 +56,7 @@ Walk walk(int N, int K, int group) {
           const int load = w4 == 1 ? h : 0, from = w4 == 1 ? t : w4 == 2 ? 2 * h + t : h;
           const int first = scale_first_group(w4, shift, run, load);
           const int have = first + scale_lane_group(w4, shift, from), want = (128 * block + 32 * w4 * t) / group;
-          for (int r = 0; r < rows; ++r)
-            if (have != want || 2 * (r * groups + have - first) + 2 > scale_records(rows, groups, first)) out.right = false;
+          if (have != want || !loaded(w4, run, load, from, whole)) out.right = false;
         }
       }
     }

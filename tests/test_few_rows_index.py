@@ -25,7 +25,7 @@ def walk(tmp_path_factory):
     (512, 256, 32, 0), (64, 4096, 64, 0), (4096, 4096, 128, 0), (33, 768, 256, 0)])
 def test_no_scale_behind_the_tensor(walk, N, K, group, reach):
     """`reach`: the bytes that the lanes of a run's missing second block would
-    read behind the last row, were it not for the descriptor's records."""
+    read behind the last row, were they not kept from it."""
     free, past, right = map(int, walk(N, K, group))
     assert (free, past, right) == (reach, 0, 1)
 
