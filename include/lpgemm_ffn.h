@@ -18,8 +18,9 @@
  *
  * Sixteen-bit tensors are binary16 or bfloat16; `type` is the type of every
  * 16-bit tensor of a call.  Sums are held in binary32; their order depends on
- * the sizes only, so equal calls give equal bits.  Infinities and NaN go the
- * way the formulas send them.
+ * the sizes and the device's number of compute units only, so equal calls on
+ * equal devices give equal bits.  Infinities and NaN go the way the formulas
+ * send them, but for rows of X at lpgemm_w4.
  *
  * Workspaces are scratch: a call writes every byte that it reads, nothing has
  * to be cleared, and nothing is kept from one call for the next.  Calls that
@@ -86,7 +87,8 @@ lpgemm_status lpgemm_dequantize_w4(int64_t N, int64_t K, int64_t group, lpgemm_t
  * weight is first rounded once to `type`, into the workspace, and the product is
  * that of 16-bit weights; a weight row that may hold values past the type's range
  * is divided by a power of two before and its sums multiplied by it after, so
- * that such weights stay finite.  M = 0 or N = 0 is a no-op; K = 0 sets C to 0.
+ * that such weights stay finite.  (Exact weights for more rows: calls of up to
+ * LPGEMM_W4_EXACT_M rows each.)  M = 0 or N = 0 is a no-op; K = 0 sets C to 0.
  * X, codes and C 16-byte aligned, scales and zeros 2-byte.  M is at most
  * LPGEMM_MAX_M_W4, N at most LPGEMM_MAX_N_W4, with below 2^24 tiles of 64 x 64 of
  * C (UNSUPPORTED_SHAPE otherwise).
@@ -116,7 +118,8 @@ lpgemm_status lpgemm_gated_w4(int64_t M, int64_t F, int64_t K, int64_t group, lp
 
 /* The gated feed-forward block with 16-bit weights, everything of `type`:
  *   [g u] = X . W_gate_up^T    X: M x D, W_gate_up: 2 F x D, gate rows first
- *   h = act(g) * u             from the binary32 sums, rounded to `type`
+ *   h = act(g) * u             from the binary32 sums, rounded to `type` (past
+ *                              binary16's 65504 to an infinity)
  *   Y = h . W_down^T           W_down: D x F, Y: M x D
  * GU, if not NULL, receives [g u] (M x 2 F, each rounded once), which the
  * backward pass reads.  D and F are multiples of 8, at most LPGEMM_MAX_D_FFN;

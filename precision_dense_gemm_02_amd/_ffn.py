@@ -3,7 +3,9 @@ with group scales, and the gated feed-forward block with its gradients.
 
 As in _moe.py, every function checks its tensors (type, shape, strides,
 device), allocates with torch what is not passed in, and calls the library's
-entry point on the current torch stream of the tensors' device.
+entry point on the current torch stream of the tensors' device.  None of them is
+part of torch's automatic differentiation: what they return carries no gradient,
+whatever their inputs require.
 """
 from __future__ import annotations
 
@@ -165,7 +167,8 @@ def gemm_w4(x, codes, scales, zeros: Optional[torch.Tensor] = None, out_dtype=No
     M x K fp16 or bf16 of the scales' type (contiguous rows, a row stride that is
     a multiple of 8); C is M x N in `out_dtype` (x's type, or fp32, fp16, bf16).
     Sums are in fp32; up to 384 rows the weights enter them exactly, beyond each
-    is rounded once to x's type.  `workspace`: uint8 scratch of
+    is rounded once to x's type (for exact weights, pass x 384 rows at a time).
+    `workspace`: uint8 scratch of
     w4_workspace_bytes(M, N, K, group) to use instead of a new allocation."""
     M, N, K, stride, group, z = _x_and_w4(x, codes, scales, zeros)
     dev, t = x.device, x.dtype
@@ -227,7 +230,8 @@ def gated_ffn(x, w_gate_up, w_down, activation: str = "silu", keep: bool = False
     8); w_gate_up: 2F x D, G's rows before U's; w_down: D x F; all of one type,
     D and F multiples of 8.  act is "silu" or "gelu" (its tanh form).  Returns y,
     M x D; with `keep` (y, gate_up), gate_up = x . w_gate_up^T, M x 2F, which
-    gated_ffn_backward takes.  `workspace`: uint8 scratch of
+    gated_ffn_backward takes: torch's automatic differentiation does not see this
+    call, and y carries no gradient.  `workspace`: uint8 scratch of
     gated_ffn_workspace_bytes(M, D, F) to use instead of a new allocation."""
     M, D, F, stride = _block(x, w_gate_up, w_down)
     act = _activation(activation)

@@ -38,7 +38,7 @@ __device__ __forceinline__ float activate(float g, int kind) {
 // logistic(a(g)): act = g p, act' = p + g a' p (1 - p).  p and 1 - p are 1 / (1 +
 // e) and e / (1 + e) with e = exp(-|a|), which neither cancels nor overflows.
 // The exponential is one instruction, off by |a| units of 2^-24: at most 2^-17
-// of the value.  Past |g| = 16 the second term of GELU's derivative is below
+// of the value, and 0 past |a| = 87.3, where it would be subnormal.  Past |g| = 16 the second term of GELU's derivative is below
 // 2^-140; clamped there, g^2 a' stays finite.
 __device__ __forceinline__ void activate_with_slope(float g, int kind, float& act, float& slope) {
   const float a = kind == kSilu ? g : gelu_argument(g);

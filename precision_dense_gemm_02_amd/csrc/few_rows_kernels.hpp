@@ -271,8 +271,10 @@ __global__ __launch_bounds__(64 * WAVES) void few_rows(FewRowsArgs p) {
 
   {
     // X into LDS: rows of whole blocks, zeros behind K, in the order the
-    // fragments need.  Its loads go out before the weights' (the last two of
-    // each thread, which is all of them for one row) and are waited for behind.
+    // fragments need.  The first two chunks of each thread (with 8 waves 8192
+    // values, with 4 waves 4096) are loaded before the weights and waited for
+    // behind their loads; what is more, one row of 14336 for one, is copied in
+    // front of both.
     const int chunks = blocks * 16;
     auto x_chunk = [&](int i) -> i32x4 {
       const int row = x_chunk_row(i, chunks), c = i - row * chunks;

@@ -75,6 +75,11 @@ int64_t workspace_bytes_of(int64_t M, int64_t D, int64_t F) {
   return Space(M, D, F, dev.cu_count).total;
 }
 
+// The forward pass.  h goes into the second product as T, which its matrix
+// instructions take: y is then 0.0023 from 64 bits in bf16 and 0.0003 in fp16
+// (root mean square, of y's), with h in binary32 0.0017 and 0.0002, most of which is
+// y's own rounding.  h in two parts, the rounded one and the rest, would take the
+// product's time twice (363 of 1130 us at 4096 x 4096 x 14336 bf16).
 template <typename T>
 lpgemm_status forward(int64_t M, int64_t D, int64_t F, int activation, const void* X, int64_t x_stride,
                       const void* w_gate_up, const void* w_down, void* GU, void* Y, uint8_t* ws, int64_t ws_bytes,
@@ -137,6 +142,8 @@ lpgemm_status forward(int64_t M, int64_t D, int64_t F, int activation, const voi
   return run_tile<T>(JOB_DOWN, q, part, part_bytes, cu_count, stream);
 }
 
+// The gradients.  dg, du and h as T: the same distances from 64 bits as in the
+// forward pass; two parts of each would take 1930 of 2500 us twice at that size.
 template <typename T>
 lpgemm_status backward(int64_t M, int64_t D, int64_t F, int activation, const void* dY, int64_t dy_stride,
                        const void* X, int64_t x_stride, const void* w_gate_up, const void* w_down, const void* GU,

@@ -179,10 +179,13 @@ __device__ __forceinline__ void lds_dma_16_at(const i32x4& rsrc, uint32_t lds_ad
 // compiler the backward pass of 4096 x 4096 x 14336 bf16 takes 2570 us, pinned
 // 2480, three K-steps ahead 2445).
 //
-// Bound by the matrix cores where there are several rounds of 256 x 256 tiles: at
-// that size dX 689 us (1396 TFLOP/s), dW_gate_up 775 (1241), dW_down 417 (1153).
-// The gradients' end reads and writes 587 MB between its products (563 us in all,
-// 372 for the product alone), and 896 tiles are 3.5 rounds of 256.  A third stage
+// Several rounds of 256 x 256 tiles keep the matrix cores busy for 69 to 79% of the
+// time (at that size gate and up 69, down 75, dX 79: 689 us, 1396 TFLOP/s), K =
+// 4096 rows in the weights' gradients for less (dW_gate_up 66: 775 us, 1241
+// TFLOP/s; dW_down 57: 417, 1153): each tile's first loads and its stores are not
+// covered by another's products.  The gradients' end reads and writes 587 MB
+// between its products (39%; 563 us in all, 372 for the product alone), and 896
+// tiles are 3.5 rounds of 256.  A third stage
 // for B (160 KB of LDS are used in all) takes 1200 us of both forward products to
 // 1171; a third for A does not fit.  Small tiles: 0.43 us a stage of 64 x 128, which
 // neither a deeper ring nor earlier fragments shorten.

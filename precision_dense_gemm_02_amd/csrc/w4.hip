@@ -58,6 +58,12 @@ struct W4Space {
   }
 };
 
+// The product through 16-bit weights.  Rounding a weight to T is what the matrix
+// instructions' operands ask for: in bf16 the output is then 0.0022 from 64 bits
+// (root mean square, of the output's), with exact weights 0.0017, most of which is
+// the output's own rounding.  Weights in two parts, the rounded one and the rest,
+// would be as good as exact ones for twice the product's time (67 of 78 us at 2048
+// x 4096 x 4096).
 template <typename T>
 lpgemm_status run_whole(int64_t group, const W4TileArgs& w, uint8_t* ws, const W4Space& space, int64_t ws_bytes,
                         int cu_count, hipStream_t stream) {

@@ -21,9 +21,12 @@ struct QuantW4Args {
 // RN(q + r (w - q s)) is the correctly rounded quotient (Markstein), three
 // operations instead of ten.
 //
-// 14336 x 4096 bf16, groups of 128: 41 us, 3.6 TB/s; the inverse to fp32 41 us,
-// 6.5 TB/s (its output stays in the caches).  The quantisation is bound by its
-// operations on each value, not by memory.
+// 14336 x 4096 bf16, groups of 128: 37 to 42 us, 3.6 to 4.0 TB/s (41 with zeros);
+// the inverse to fp32 41 to 52 us, 5.2 to 6.5 TB/s (part of its output stays in the
+// caches).  The quantisation spends its time on the 25 vector operations that it
+// has for each value, not on memory.  That is not the least: a branch per code, a
+// zero that is added where there is none, masks and shifts apart and a division
+// per lane are in them.
 template <typename T, int LANES, bool ZEROS>
 __global__ __launch_bounds__(256) void quantize_w4_kernel(QuantW4Args p) {
   const uint32_t i = blockIdx.x * 256u + threadIdx.x;

@@ -22,14 +22,18 @@ struct W4Plan {
 };
 
 // Up to this many rows the weights enter the sums exactly; beyond, they are
-// first written out as 16-bit values, each rounded once.
+// first written out as 16-bit values, each rounded once.  The tiles with exact
+// weights against that, in us: 32 rows x 14336 x 4096 21 and 62; 256 rows x 4096 x 14336 63 and 91, x 14336 x 4096
+// 76 and 94, gated x 14336 x 4096 129 and 140; 384 rows 102 and 103, 114 and 99,
+// 192 and 166; 512 rows 114 and 129, 152 and 102, 237 and 162; 1024 rows 224 and
+// 146, 272 and 143, 468 and 266.  (4096 x 4096: 384 rows 32 and 37, 512 34 and 38,
+// 768 64 and 59, 2048 127 and 78.)
 constexpr int kW4ExactRows = LPGEMM_W4_EXACT_M;
 
 // N: weight rows (gated: both projections').  In us, few rows' kernel against the
 // best tiles: 16 x 4096 x 4096 8.7 and 11.5, 16 x 14336 x 4096 18.6 and 19.9, but
 // 16 x 28672 x 4096 30.1 and 22.8; 32 x 4096 x 4096 11.9 and 12.7, but 32 x 4096 x
-// 14336 33.2 and 20.5.  Tiles against 16-bit weights: 32 x 14336 x 4096 21.0 and
-// 59.6, 2048 x 4096 x 4096 577 and 76.
+// 14336 33.2 and 20.5.  Tiles against 16-bit weights: at kW4ExactRows.
 inline W4Plan plan_w4(int64_t M, int64_t N, int64_t K, int cu_count) {
   const int64_t weights = N * K;
   W4Plan plan{W4_TILE, 32, 1};

@@ -61,6 +61,24 @@ DEFAULT_KERNELS = {
     "lpgemm::grouped_tile<6, 128, 128, 2, 2, 2, false, true, true>": "MXFP4 experts of 32 rows, B non-temporal",
     "lpgemm::grouped_tile<3, 256, 256, 2, 2, 2, true, true, false>": "int8 experts of 1024 rows",
     "lpgemm::grouped_tile<6, 256, 256, 2, 2, 2, true, true, false>": "MXFP4 8192^3",
+    "lpgemm::quantize_w4_kernel<lpgemm::TypeBF16, 16, false>": "4-bit weights in groups of 128, 14336 x 4096",
+    "lpgemm::dequantize_w4_kernel<lpgemm::TypeBF16, 0>": "4-bit weights' values as binary32, 14336 x 4096",
+    "lpgemm::rows_w4_kernel<lpgemm::TypeBF16>": "4-bit weights as rows of a product of more than 384 rows",
+    "lpgemm::few_rows<lpgemm::TypeF16, 4, false, 1, 1, true, 8, 4>": "4-bit weights, one token, 4096 x 14336",
+    "lpgemm::few_rows<lpgemm::TypeBF16, 4, false, 1, 2, true, 8, 2>": "4-bit weights, one token, gate and up projections",
+    "lpgemm::few_rows<lpgemm::TypeBF16, 2, true, 1, 4, false, 8, 1>": "4-bit weights in groups of 64 with zeros, 16 rows",
+    "lpgemm::few_rows<lpgemm::TypeF16, 1, true, 2, 2, false, 8, 1>": "4-bit weights in groups of 32 with zeros, 37 rows",
+    "lpgemm::few_rows<lpgemm::TypeBF16, 0, false, 1, 2, true, 8, 3>": "the block's gate and up projections, one token",
+    "lpgemm::few_rows<lpgemm::TypeBF16, 0, false, 1, 1, true, 8, 4>": "the block's down projection, one token",
+    "lpgemm::w4_tile<lpgemm::TypeBF16, 4, 32, 2, 4, false>": "4-bit weights, 32 rows x 14336 x 4096",
+    "lpgemm::w4_tile<lpgemm::TypeBF16, 4, 64, 2, 2, false>": "4-bit weights, 128 rows x 14336 x 4096",
+    "lpgemm::ffn_tile<lpgemm::TypeBF16, false, false, 128, 128, 2, 2, 2, 3, 0, true>": "4-bit weights, 2048 x 4096 x 4096",
+    "lpgemm::ffn_tile<lpgemm::TypeF16, false, false, 256, 256, 2, 2, 2, 3, 1, false>": "the block's gate and up projections, 4096 x 4096 x 14336",
+    "lpgemm::ffn_tile<lpgemm::TypeF16, false, false, 256, 256, 2, 2, 2, 3, 0, false>": "the block's down projection, 4096 x 4096 x 14336",
+    "lpgemm::ffn_tile<lpgemm::TypeBF16, false, false, 64, 128, 2, 2, 3, 3, 1, false>": "the block's gate and up projections, 511 x 2056 x 1416",
+    "lpgemm::ffn_tile<lpgemm::TypeBF16, false, true, 256, 256, 2, 2, 2, 3, 2, false>": "dh and the activation's gradient, 4096 x 4096 x 14336",
+    "lpgemm::ffn_tile<lpgemm::TypeBF16, false, true, 256, 256, 2, 2, 2, 3, 0, false>": "dX of that block",
+    "lpgemm::ffn_tile<lpgemm::TypeBF16, true, true, 256, 256, 2, 2, 2, 3, 0, false>": "its weights' gradients",
 }
 FIELDS = ["VGPRs", "AGPRs", "TotalSGPRs", "ScratchSize [bytes/lane]", "LDS Size [bytes/block]",
           "Occupancy [waves/SIMD]", "VGPRs Spill"]
