@@ -90,21 +90,30 @@ __device__ __forceinline__ void finish8_grad(const TileArgs& p, int row, int col
   *(i32x4*)(p.H + 2 * ((size_t)row * p.F + col)) = narrow8<T>(h);
 }
 
-// (places up to the next multiple of eight columns hold a factor, too)
-__device__ __forceinline__ void multiply8(float (&v)[8], const float* factors) {
-  const f32x4 a = *(const f32x4*)factors, b = *(const f32x4*)(factors + 4);
+// Eight columns' factors, gate's and up's: loaded ahead of the sums.  (Places up to
+// the next multiple of eight columns hold one, too.)
+struct Factors8 {
+  f32x4 g[2], u[2];
+  template <int END>
+  __device__ __forceinline__ void load(const TileArgs& p, int col) {
+    const float* at = p.factors + col;
+    g[0] = *(const f32x4*)at, g[1] = *(const f32x4*)(at + 4);
+    if constexpr (END == END_GATED) at += p.part_stride / 2, u[0] = *(const f32x4*)at, u[1] = *(const f32x4*)(at + 4);
+  }
+  template <int END>
+  __device__ __forceinline__ void multiply(float (&v)[8], float (&w)[8]) const {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) v[e] *= a[e], v[4 + e] *= b[e];
-}
+    for (int e = 0; e < 8; ++e) {
+      v[e] *= g[e / 4][e % 4];
+      if constexpr (END == END_GATED) w[e] *= u[e / 4][e % 4];
+    }
+  }
+};
 
 // Eight consecutive columns of one row: what END does with them.  `v`: the sums
 // (END_GATED: of the gate), `u`: those of the up projection.
-template <typename T, int END, bool FACTORS>
-__device__ __forceinline__ void finish8(const TileArgs& p, int row, int col, float (&v)[8], float (&u)[8]) {
-  if constexpr (FACTORS) {
-    multiply8(v, p.factors + col);
-    if constexpr (END == END_GATED) multiply8(u, p.factors + p.part_stride / 2 + col);
-  }
+template <typename T, int END>
+__device__ __forceinline__ void finish8(const TileArgs& p, int row, int col, const float (&v)[8], const float (&u)[8]) {
   if constexpr (END == END_STORE) {
     store_columns(p.C, p.out_type, row, col, p.N, v);
   } else if constexpr (END == END_GATED) {
@@ -131,6 +140,8 @@ __global__ __launch_bounds__(256) void join_splits(TileArgs p) {
   const int chunks = (columns + 7) / 8;
   const int row = (int)(i / chunks), col = 8 * (int)(i - (int64_t)row * chunks);
   if (row >= p.M) return;
+  Factors8 factors;
+  if constexpr (FACTORS) factors.template load<END>(p, col);
   float v[8] = {}, u[8] = {};
   for (int s = 0; s < p.splits; ++s) {
     const float* part = p.part + ((size_t)s * p.M + row) * p.part_stride + col;
@@ -146,7 +157,8 @@ __global__ __launch_bounds__(256) void join_splits(TileArgs p) {
       }
     }
   }
-  finish8<T, END, FACTORS>(p, row, col, v, u);
+  if constexpr (FACTORS) factors.template multiply<END>(v, u);
+  finish8<T, END>(p, row, col, v, u);
 }
 
 template <typename F, int... T>
@@ -194,7 +206,8 @@ __device__ __forceinline__ void lds_dma_16_at(const i32x4& rsrc, uint32_t lds_ad
 // projection, so that both sums of an element meet in one lane.
 //
 // FACTORS: B's rows were divided by powers of two (4-bit weights); the sums are
-// multiplied by them again.  A choice at compile time, in translation units of
+// multiplied by them again, which are loaded in front of the main loop (2048 x 64 x
+// 256 7.7 -> 7.0 us).  A choice at compile time, in translation units of
 // their own: a test of the pointer at run time costs every other product 1 to 5%
 // (forward 1024 x 2048 x 5632 86.6 -> 90.8 us), and the same code object its
 // neighbours up to 4% (backward of that size 210 -> 218).
@@ -393,6 +406,14 @@ __global__ __launch_bounds__(256) void ffn_tile(TileArgs p) {
     slot_b = next_b;
   };
 
+  constexpr int kBlocks = GATED ? TN / 2 : TN;   // column blocks of C
+  const int wave_col = n0 + wn * (GATED ? WTN / 2 : WTN) + 8 * fh;
+  Factors8 factors[FACTORS ? 2 * kBlocks : 1];   // (the loads land behind the main loop)
+  if constexpr (FACTORS) {
+#pragma unroll
+    for (int c = 0; c < 2 * kBlocks; ++c) factors[c].template load<END>(p, wave_col + 16 * c < columns ? wave_col + 16 * c : 0);
+  }
+
   if (s_begin < s_end) {
     // the loads that the rounds before would have sent
 #pragma unroll
@@ -414,8 +435,6 @@ __global__ __launch_bounds__(256) void ffn_tile(TileArgs p) {
   // The matrix instructions have B's rows as theirs: a lane holds one row of C,
   // and of its columns four at a time, 8 q + 4 (l / 32) .. + 3 of each 32.  Two
   // such runs, exchanged between the half-waves, are eight consecutive columns.
-  constexpr int kBlocks = GATED ? TN / 2 : TN;   // column blocks of C
-  const int wave_col = n0 + wn * (GATED ? WTN / 2 : WTN) + 8 * fh;
   auto eight = [&](const f32x16& x, int q, float (&v)[8]) __attribute__((always_inline)) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -463,7 +482,8 @@ __global__ __launch_bounds__(256) void ffn_tile(TileArgs p) {
       } else if constexpr (END == END_GATED_GRAD) {
         finish8_grad<T>(p, row, col, v, kept[2 * c], kept[2 * c + 1]);
       } else {
-        finish8<T, END, FACTORS>(p, row, col, v, u);
+        if constexpr (FACTORS) factors[c].template multiply<END>(v, u);
+        finish8<T, END>(p, row, col, v, u);
       }
     }
   }

@@ -125,8 +125,8 @@ struct RowsW4Args {
 };
 
 // Weights as values of T, each rounded once, for a product behind them.  A
-// weight may lie past T's range (a scale of 5000 with code 14 of a zero of -7,
-// in binary16), where rounding would make it an infinity and the sums with it:
+// weight may lie past T's range (a scale of 5000, code 7 and a zero of -7, in
+// binary16), where rounding would make it an infinity and the sums with it:
 // such a row is divided by a power of two, factors[row], which its sums are
 // multiplied by again.  |weight| < 2^(a + b) for |scale| < 2^a and |zero| + 8 <
 // 2^b, the largest a + b of a row's groups decides; most rows have factor 1 and
@@ -134,10 +134,10 @@ struct RowsW4Args {
 // stay out of the choice and go into their group's values.
 //
 // A wave takes 4096 values of a row and finds the row's factor itself, behind
-// the loads of its first codes: 4096 x 4096 in groups of 128 9.5 us, 14336 x 4096
-// in groups of 64 with zeros 24.3 (dequantize_w4_kernel, without factors, 8.4 and
-// 23.2).  With the factors' way into the sums a product of 2048 x 4096 x 4096 takes
-// 80 us instead of 78, the smallest ones 1.6 us more.
+// the loads of its codes and their scales: 4096 x 4096 in groups of 128 8.7 us, 14336
+// x 4096 in groups of 64 with zeros 25.1 (dequantize_w4_kernel, without factors, 8.4
+// and 23.2).  With the factors' way into the sums a product of 2048 x 4096 x 4096
+// takes 79 us instead of 78, the smallest ones 0.8 us more.
 template <typename T>
 __global__ __launch_bounds__(256) void rows_w4_kernel(RowsW4Args p) {
   constexpr int kMost = kIsF16<T> ? 15 : 127;   // |weight| below 2^kMost is in range after rounding
@@ -156,33 +156,43 @@ __global__ __launch_bounds__(256) void rows_w4_kernel(RowsW4Args p) {
   const uint32_t* const codes = (const uint32_t*)p.codes + row * p.chunks;
   const uint16_t* const scales = p.scales + row * p.groups;
   const uint16_t* const zeros = p.zeros ? p.zeros + row * p.groups : nullptr;
-  uint32_t packed[kEach];
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) packed[i] = first + 64 * i < p.chunks ? codes[first + 64 * i] : 0;
   auto exponent = [](float v) { return (int)(__builtin_bit_cast(uint32_t, v) >> 23 & 255) - 126; };   // |v| < 2^it
-  int most = -1000;
-  for (int g = lane; g < p.groups; g += 64) {
-    const int a = exponent(widen1<T>(scales[g])), b = exponent(zeros ? __builtin_fabsf(widen1<T>(zeros[g])) + 8.f : 8.f);
-    if (a < 129 && b < 129) most = max(most, a + b);     // (129: infinities and NaN)
-  }
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) most = max(most, __shfl_xor(most, off));
-  const int e = min(max(most - kMost, 0), 126);
   auto power = [](int n) { return __builtin_bit_cast(float, (uint32_t)(127 + n) << 23); };
-  if (blockIdx.y == 0 && lane == 0) p.factors[at] = power(e);
-  const float down = power(-e);
+  auto run = [&](auto whole_c) __attribute__((always_inline)) {   // all of the wave's places hold chunks
+    constexpr bool whole = decltype(whole_c)::value;
+    uint32_t packed[kEach];
+    uint16_t scale[kEach], zero[kEach];
 #pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const int c = first + 64 * i;
-    if (c >= p.chunks) break;
-    const int group = c >> p.lanes_log2;
-    const float s = __fmul_rn(widen1<T>(scales[group]), down);
-    const float z = zeros ? widen1<T>(zeros[group]) : 0.f;
-    float v[8];
+    for (int i = 0; i < kEach; ++i) {
+      const int c = first + 64 * i;
+      if (!whole && c >= p.chunks) break;
+      packed[i] = codes[c];
+      scale[i] = scales[c >> p.lanes_log2];
+      zero[i] = zeros ? zeros[c >> p.lanes_log2] : 0;
+    }
+    int most = -1000;
+    for (int g = lane; g < p.groups; g += 64) {
+      const int a = exponent(widen1<T>(scales[g])), b = exponent(zeros ? __builtin_fabsf(widen1<T>(zeros[g])) + 8.f : 8.f);
+      if (a < 129 && b < 129) most = max(most, a + b);     // (129: infinities and NaN)
+    }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = __fmul_rn((float)((int)(packed[i] << (28 - 4 * k)) >> 28) - z, s);
-    *(i32x4*)(p.Y + 16 * (row * p.chunks + c)) = narrow8<T>(v);
-  }
+    for (int off = 1; off < 64; off <<= 1) most = max(most, __shfl_xor(most, off));
+    const int e = min(max(most - kMost, 0), 126);
+    if (blockIdx.y == 0 && lane == 0) p.factors[at] = power(e);
+    const float down = power(-e);
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int c = first + 64 * i;
+      if (!whole && c >= p.chunks) break;
+      const float s = __fmul_rn(widen1<T>(scale[i]), down), z = widen1<T>(zero[i]);
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = __fmul_rn((float)((int)(packed[i] << (28 - 4 * k)) >> 28) - z, s);
+      *(i32x4*)(p.Y + 16 * (row * p.chunks + c)) = narrow8<T>(v);
+    }
+  };
+  if (p.chunks - (int)blockIdx.y * (64 * kEach) >= 64 * kEach) run(std::true_type());
+  else run(std::false_type());
 }
 
 }  // namespace lpgemm
